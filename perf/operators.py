@@ -1,0 +1,375 @@
+"""The adapter and balance operators as they are measured: the int4 projection
+with low-rank adapters of many requests (forward and backward) and the router's
+balance loss with its per-expert counts (forward and backward).
+
+Each case is one call.  `run` computes it in elementary torch operations, or,
+where `own` is true, through the library's entry points on the same inputs.
+`exact` evaluates the definitions in 64 bits.
+
+Definitions.
+  Projection, per token t with adapter a = adapter[t] (none if outside [0, n)):
+    x^ = Q8_0(x_t): per 32-block d = amax / 127, q = round-half-even(x / d),
+         both in 32-bit arithmetic (that is the format), x^ = q d
+    W^ = int4 weights times their group scale (64 weights of a row per scale)
+    u_t = A_a x_t,    out_t = W^ x^_t + scale_a B_a u_t
+  Its gradients for an upstream g (the rounding of x to Q8_0 passes gradients
+  unchanged, W^ is frozen), v_t = scale_a B_a' g_t:
+    dx_t = W^' g_t + A_a' v_t
+    dA_a = sum over its tokens of v_t x_t',  dB_a = sum of scale_a g_t u_t'
+  Balance loss of segment s with n_s counted tokens, p = softmax(logits):
+    counts[s][e] = kept pairs on expert e,  f = counts E / (k n_s)
+    pmean[s][e]  = sum of p[t][e] / n_s,    loss_s = sum_e f_e pmean_e
+  (0 where n_s = 0) and, for upstream dloss_s and the gradient dw of the kept
+  weights w (softmax over the kept logits),
+    dlogits[t][e] = dloss_s / n_s p_e (f_e - sum_j f_j p_j)
+                    + sum over slots i with idx[t][i] = e of w_i (dw_i - sum_j w_j dw_j)
+"""
+import math
+
+import torch
+
+own = False
+
+GROUP, BLOCK = 64, 32  # int4 weights per scale, activations per scale
+
+
+def listed():
+    return [
+        # one token of one request through the adapted gate (or up) matrix of
+        # the shared expert: the call a single-user decode step makes
+        {"name": "lora_t1", "op": "lora_fwd", "T": 1, "K": 6144, "N": 2048, "n": 16, "r": 16, "fp16": False, "save": False},
+        # a decode batch of 16 requests, most with an adapter of their own, through the down matrix
+        {"name": "lora_t16_down", "op": "lora_fwd", "T": 16, "K": 2048, "N": 6144, "n": 16, "r": 16, "fp16": False, "save": False},
+        # a ragged mixed batch: decode tokens of many requests beside a few short prompts
+        {"name": "lora_t203_mixed", "op": "lora_fwd", "T": 203, "K": 6144, "N": 2048, "n": 24, "r": 32, "fp16": True, "save": False},
+        # the prompts of a prefill batch, and the forward of a fine-tuning step (A x kept for the backward)
+        {"name": "lora_t2048", "op": "lora_fwd", "T": 2048, "K": 6144, "N": 2048, "n": 8, "r": 64, "fp16": False, "save": True},
+        # the backward of a small fine-tuning batch of four adapters
+        {"name": "lora_bwd_t512", "op": "lora_bwd", "T": 512, "K": 6144, "N": 2048, "n": 4, "r": 16, "fp16": False, "save": True},
+        # the backward of a full fine-tuning batch through the down matrix
+        {"name": "lora_bwd_t2048_down", "op": "lora_bwd", "T": 2048, "K": 2048, "N": 6144, "n": 8, "r": 64, "fp16": True, "save": True},
+        # the balance record of one decode batch
+        {"name": "balance_t16", "op": "bal_fwd", "T": 16, "S": 1, "E": 256, "k": 8, "mask": False},
+        # the packed sequences of one prefill batch, padding rows and dropped pairs among them
+        {"name": "balance_t2048_seqs", "op": "bal_fwd", "T": 2048, "S": 5, "E": 256, "k": 8, "mask": True},
+        # a global batch of a fine-tuning step
+        {"name": "balance_t131072", "op": "bal_fwd", "T": 131072, "S": 1, "E": 256, "k": 8, "mask": False},
+        # the gradient of the prefill batch, the kept weights' gradient with it
+        {"name": "balance_bwd_t2048", "op": "bal_bwd", "T": 2048, "S": 5, "E": 256, "k": 8, "mask": True, "dw": True},
+        # a router with a count of experts that no vector width divides
+        {"name": "balance_bwd_t777_e90", "op": "bal_bwd", "T": 777, "S": 3, "E": 90, "k": 6, "mask": True, "dw": True},
+        # the gradient of a global batch, a loss per sequence
+        {"name": "balance_bwd_t131072", "op": "bal_bwd", "T": 131072, "S": 32, "E": 256, "k": 8, "mask": False, "dw": True},
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["lora_fwd", "lora_fwd", "lora_bwd", "bal_fwd", "bal_bwd"])
+    if op.startswith("lora"):
+        T = _log_int(rng, 1, 2048)
+        K = GROUP * _log_int(rng, 2, 96)
+        N = 8 * _log_int(rng, 8, 768)
+        if K * N > 6144 * 2048:  # no larger than the layer's own matrices
+            N = max(8, 6144 * 2048 // K // 8 * 8)
+        return {"op": op, "T": T, "K": K, "N": N, "n": _log_int(rng, 1, 32), "r": 8 * rng.randint(1, 8),
+                "fp16": rng.random() < 0.5, "save": rng.random() < 0.5}
+    T = _log_int(rng, 1, 131072)
+    E = _log_int(rng, 8, 256)
+    c = {"op": op, "T": T, "S": _log_int(rng, 1, 32), "E": E, "k": rng.randint(1, min(8, E)),
+         "mask": rng.random() < 0.5}
+    if op == "bal_bwd":
+        c["dw"] = rng.random() < 0.7
+    return c
+
+
+def work(case):
+    T = case["T"]
+    if case["op"].startswith("lora"):
+        K, N, n, r = case["K"], case["N"], case["n"], case["r"]
+        W = N * K // 2 + N * K // GROUP * 2
+        used = min(n, T) * r * (K + N) * 2  # the adapters that the tokens can name
+        if case["op"] == "lora_fwd":
+            return {"bytes": 4 * T * K + W + used + 4 * T * N + 4 * T + (4 * T * r if case["save"] else 0),
+                    "flops": 2 * T * (N * K + r * (K + N))}
+        u = 4 * T * r if case["save"] else 0
+        more = 0 if case["save"] else 2 * T * r * K  # u computed again
+        return {"bytes": 8 * T * K + 4 * T * N + W + used + u + 4 * T + 4 * n * r * (K + N),
+                "flops": 2 * T * (N * K + 2 * r * (K + N)) + more}
+    S, E, k = case["S"], case["E"], case["k"]
+    if case["op"] == "bal_fwd":
+        return {"bytes": 4 * T * E + 4 * T * k + 8 * S * E + 8 * S + (T if case["mask"] else 0), "flops": 5 * T * E}
+    return {"bytes": 8 * T * E + 4 * S * E + 8 * S + (12 * T * k if case["dw"] else 0) + (T if case["mask"] else 0),
+            "flops": 8 * T * E}
+
+
+# ---------------------------------------------------------------------- inputs
+def _prepare_lora(case, g, dev):
+    T, K, N, n, r = case["T"], case["K"], case["N"], case["n"], case["r"]
+    dt = torch.float16 if case["fp16"] else torch.bfloat16
+
+    def randn(*shape):
+        return torch.randn(shape, generator=g, device=dev)
+
+    packed = torch.randint(0, 256, (N * K // 2,), generator=g, device=dev, dtype=torch.uint8)
+    scales = torch.exp(randn(N * K // GROUP) * 0.3 + math.log(0.02)).to(torch.float16)
+    s = {"T": T, "K": K, "N": N, "n": n, "r": r, "x": randn(T, K),
+         "W": torch.cat([packed, scales.view(torch.uint8)]),
+         "A": (randn(n, r, K) / math.sqrt(K)).to(dt), "B": (randn(n, N, r) * 0.05).to(dt),
+         "scale": torch.rand(n, generator=g, device=dev) * 1.5 + 0.5,
+         # one request in eight or so brings no adapter; the rest fall on the
+         # adapters unevenly
+         "adapter": (torch.rand(T, generator=g, device=dev) ** 1.5 * (n + 0.13 * n) - 0.13 * n).floor().clamp_(-1, n - 1).to(torch.int32)}
+    if case["op"] == "lora_bwd":
+        s["g"] = randn(T, N) * 1e-3
+        s["u"] = None
+        if case["save"]:  # A x of each token, as the forward call left it
+            ua = (s["x"].double() @ s["A"].double().reshape(n * r, K).t()).view(T, n, r)
+            a = s["adapter"].long()
+            s["u"] = (ua[torch.arange(T, device=dev), a.clamp(min=0)] * (a >= 0)[:, None]).float()
+        s["dx"] = torch.empty(T, K, device=dev)
+        s["dA"] = torch.empty(n, r, K, device=dev)
+        s["dB"] = torch.empty(n, N, r, device=dev)
+    else:
+        s["out"] = torch.empty(T, N, device=dev)
+        s["u"] = torch.empty(T, r, device=dev) if case["save"] else None
+    return s
+
+
+def _prepare_balance(case, g, dev):
+    T, S, E, k = case["T"], case["S"], case["E"], case["k"]
+    # skewed popularity, as a router that needs balancing has it
+    bias = torch.randn(E, generator=g, device=dev)
+    logits = torch.randn(T, E, generator=g, device=dev) * 1.5 + bias
+    top, idx = torch.sort(logits, dim=1, descending=True, stable=True)
+    top, idx = top[:, :k], idx[:, :k].to(torch.int32)
+    s = {"T": T, "S": S, "E": E, "k": k, "logits": logits, "idx": idx.contiguous(),
+         "seg": None, "valid": None, "w": None, "dw": None}
+    if S > 1:  # packed sequences of uneven lengths; some may be empty
+        cuts = torch.sort(torch.randint(0, T + 1, (S - 1,), generator=g, device=dev)).values
+        s["seg"] = torch.cat([cuts.new_zeros(1), cuts, cuts.new_full((1,), T)]).to(torch.int32)
+    if case["mask"]:
+        s["valid"] = (torch.rand(T, generator=g, device=dev) > 0.07).to(torch.uint8)
+        s["idx"][torch.rand(T, k, generator=g, device=dev) < 0.02] = -1  # pairs over an expert's capacity
+    if case["op"] == "bal_fwd":
+        s["counts"] = torch.empty(S, E, dtype=torch.int32, device=dev)
+        s["ntok"] = torch.empty(S, dtype=torch.int32, device=dev)
+        s["pmean"] = torch.empty(S, E, device=dev)
+        s["loss"] = torch.empty(S, device=dev)
+        return s
+    # what the forward call left, and the upstream gradients
+    sid, member = _members(s)
+    s["counts"], s["ntok"] = _counts(s, sid, member)
+    s["dloss"] = torch.randn(S, generator=g, device=dev) * 0.3 + 1.0
+    if case["dw"]:
+        s["w"] = torch.softmax(top, dim=1).contiguous()
+        s["dw"] = torch.randn(T, k, generator=g, device=dev) * 1e-3
+    s["dlogits"] = torch.empty(T, E, device=dev)
+    return s
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(int(seed))
+    s = _prepare_lora(case, g, dev) if case["op"].startswith("lora") else _prepare_balance(case, g, dev)
+    s["op"] = case["op"]
+    return s
+
+
+# ----------------------------------------------------------------- plain forms
+def _dequantised(s):
+    N, K = s["N"], s["K"]
+    b = s["W"][: N * K // 2].view(N, K // GROUP, GROUP // 2)
+    w = torch.cat([b & 15, b >> 4], dim=2).float() - 8.0
+    sc = s["W"][N * K // 2:].view(torch.float16).view(N, K // GROUP, 1).float()
+    return (w * sc).view(N, K)
+
+
+def _q8_0(x):
+    b = x.view(x.shape[0], -1, BLOCK)
+    d = b.abs().amax(dim=2, keepdim=True) / 127.0
+    q = torch.where(d > 0, torch.round(b / d), torch.zeros_like(b)).clamp(-127, 127)
+    return (q * d).view_as(x)
+
+
+def _own_adapter(s):
+    """[T][n r]: scale_a in the columns of the token's adapter, else 0."""
+    hot = s["adapter"][:, None] == torch.arange(s["n"], device=s["adapter"].device)
+    return (hot * s["scale"]).repeat_interleave(s["r"], dim=1)
+
+
+def _lora_fwd(s):
+    n, r, K, N = s["n"], s["r"], s["K"], s["N"]
+    A = s["A"].float().reshape(n * r, K)
+    B = s["B"].float().permute(0, 2, 1).reshape(n * r, N)
+    ua = s["x"] @ A.t()
+    out = _q8_0(s["x"]) @ _dequantised(s).t() + (ua * _own_adapter(s)) @ B
+    if s["u"] is None:
+        return out
+    a = s["adapter"].long()
+    u = ua.view(-1, n, r)[torch.arange(s["T"], device=a.device), a.clamp(min=0)] * (a >= 0)[:, None]
+    return out, u
+
+
+def _lora_bwd(s):
+    n, r, K, N = s["n"], s["r"], s["K"], s["N"]
+    A = s["A"].float().reshape(n * r, K)
+    B = s["B"].float().permute(0, 2, 1).reshape(n * r, N)
+    mask = _own_adapter(s)
+    v = (s["g"] @ B.t()) * mask
+    dx = s["g"] @ _dequantised(s) + v @ A
+    u = s["x"] @ A.t() if s["u"] is None else s["u"].repeat(1, n)
+    return dx, (v.t() @ s["x"]).view(n, r, K), ((u * mask).t() @ s["g"]).view(n, r, N).permute(0, 2, 1).contiguous()
+
+
+def _members(s):
+    """Segment of each token, and [S][T] which tokens each segment counts."""
+    T, S = s["T"], s["S"]
+    t = torch.arange(T, device=s["idx"].device)
+    sid = torch.zeros_like(t) if s["seg"] is None else torch.searchsorted(s["seg"][1:].long(), t, right=True)
+    member = sid == torch.arange(S, device=t.device)[:, None]
+    return sid, member if s["valid"] is None else member & (s["valid"] > 0)
+
+
+def _counts(s, sid, member):
+    S, E = s["S"], s["E"]
+    live = member.any(dim=0)[:, None] & (s["idx"] >= 0)
+    at = (sid[:, None] * E + s["idx"].long())[live]
+    counts = torch.zeros(S * E, dtype=torch.int32, device=at.device)
+    counts.index_add_(0, at, torch.ones_like(at, dtype=torch.int32))
+    return counts.view(S, E), member.sum(dim=1).to(torch.int32)
+
+
+def _probabilities(logits):
+    m = logits.amax(dim=1, keepdim=True)
+    e = torch.exp(logits - m)
+    return e / e.sum(dim=1, keepdim=True)
+
+
+def _balance_fwd(s):
+    sid, member = _members(s)
+    counts, ntok = _counts(s, sid, member)
+    n = ntok.clamp(min=1).float()[:, None]
+    pmean = (member.float() @ _probabilities(s["logits"])) / n
+    f = counts.float() * s["E"] / (s["k"] * n)
+    return counts, ntok, pmean, (f * pmean).sum(dim=1)
+
+
+def _balance_bwd(s):
+    sid, member = _members(s)
+    p = _probabilities(s["logits"])
+    n = s["ntok"].clamp(min=1).float()
+    f = (s["counts"].float() * s["E"] / (s["k"] * n[:, None]))[sid]
+    c = (s["dloss"] / n)[sid][:, None] * member.any(dim=0)[:, None]
+    d = c * p * (f - (f * p).sum(dim=1, keepdim=True))
+    if s["w"] is not None:
+        kept = s["w"] * (s["dw"] - (s["w"] * s["dw"]).sum(dim=1, keepdim=True))
+        live = s["idx"] >= 0
+        d.scatter_add_(1, s["idx"].long().clamp(min=0), kept * live)
+    return d
+
+
+# ------------------------------------------------------------- the library's calls
+def _own(s):
+    import int4_routed_expert_softmax_b200 as moe
+    op = s["op"]
+    if op.startswith("lora"):
+        if "plan" not in s:  # kept by a user's program beside its weights
+            s["plan"] = moe.lora(s["K"], s["N"], s["n"], s["r"], s["A"].dtype)
+            s["ws"] = moe.alloc_lora_workspace(s["plan"], s["T"], backward=op == "lora_bwd")
+        if op == "lora_fwd":
+            moe.moe_lora_forward(s["plan"], s["x"], s["W"], s["A"], s["B"], s["scale"], s["adapter"], s["out"], s["ws"], u=s["u"])
+            return s["out"] if s["u"] is None else (s["out"], s["u"])
+        moe.moe_lora_backward(s["plan"], s["g"], s["x"], s["W"], s["A"], s["B"], s["scale"], s["adapter"], s["ws"],
+                              u=s["u"], dx=s["dx"], dA=s["dA"], dB=s["dB"])
+        return s["dx"], s["dA"], s["dB"]
+    if "plan" not in s:
+        s["plan"] = moe.dims(6144, 2048, s["E"], s["k"])
+        s["ws"] = moe.alloc_balance_workspace(s["plan"], s["T"], s["S"]) if op == "bal_fwd" else None
+    if op == "bal_fwd":
+        moe.moe_balance_forward(s["plan"], s["logits"], s["idx"], s["counts"], s["ntok"], s["pmean"], s["loss"], s["ws"],
+                                seg=s["seg"], valid=s["valid"])
+        return s["counts"], s["ntok"], s["pmean"], s["loss"]
+    moe.moe_balance_backward(s["plan"], s["logits"], s["idx"], s["counts"], s["ntok"], s["dloss"], s["dlogits"],
+                             seg=s["seg"], valid=s["valid"], w=s["w"], dw=s["dw"])
+    return s["dlogits"]
+
+
+def run(state):
+    if own:
+        return _own(state)
+    return {"lora_fwd": _lora_fwd, "lora_bwd": _lora_bwd, "bal_fwd": _balance_fwd, "bal_bwd": _balance_bwd}[state["op"]](state)
+
+
+# ------------------------------------------------------------------ in 64 bits
+def exact(case, seed):
+    s = prepare(case, seed)
+    T = s["T"]
+    f64 = torch.float64
+    if case["op"].startswith("lora"):
+        K, N, n, r = s["K"], s["N"], s["n"], s["r"]
+        raw = s["W"][: N * K // 2].to(torch.int64).view(N, K // GROUP, 1, GROUP // 2)
+        nib = torch.stack([raw[:, :, 0] % 16, raw[:, :, 0] // 16], dim=2).reshape(N, K // GROUP, GROUP) - 8
+        What = (nib.to(f64) * s["W"][N * K // 2:].view(torch.float16).to(f64).view(N, K // GROUP, 1)).reshape(N, K)
+        x, ids = s["x"].to(f64), s["adapter"].long()
+        sc = s["scale"].to(f64)
+        rows = [torch.nonzero(ids == a).flatten() for a in range(n)]
+        if case["op"] == "lora_fwd":
+            # the codes follow from 32-bit arithmetic by definition; their values do not
+            xb = s["x"].view(T, K // BLOCK, BLOCK)
+            d = xb.abs().max(dim=2).values / 127.0
+            q = torch.nan_to_num(torch.round(xb / d[:, :, None]), nan=0.0).clamp(-127, 127)
+            out = (q.to(f64) * d.to(f64)[:, :, None]).reshape(T, K) @ What.t()
+            u = torch.zeros(T, r, dtype=f64, device=x.device)
+            for a in range(n):
+                u[rows[a]] = x[rows[a]] @ s["A"][a].to(f64).t()
+                out[rows[a]] += sc[a] * (u[rows[a]] @ s["B"][a].to(f64).t())
+            return (out, u) if s["u"] is not None else out
+        g = s["g"].to(f64)
+        dx = g @ What
+        dA = torch.zeros(n, r, K, dtype=f64, device=x.device)
+        dB = torch.zeros(n, N, r, dtype=f64, device=x.device)
+        for a in range(n):
+            i = rows[a]
+            Aa, Ba = s["A"][a].to(f64), s["B"][a].to(f64)
+            v = sc[a] * (g[i] @ Ba)
+            u = x[i] @ Aa.t() if s["u"] is None else s["u"][i].to(f64)
+            dx[i] += v @ Aa
+            dA[a] = v.t() @ x[i]
+            dB[a] = sc[a] * (g[i].t() @ u)
+        return dx, dA, dB
+    S, E, k = s["S"], s["E"], s["k"]
+    bounds = [0, T] if s["seg"] is None else s["seg"].tolist()
+    idx = s["idx"].long()
+    valid = torch.ones(T, dtype=torch.bool, device=idx.device) if s["valid"] is None else s["valid"].bool()
+    p = torch.softmax(s["logits"].to(f64), dim=1)
+    counts = torch.zeros(S, E, dtype=torch.int32, device=idx.device)
+    ntok = torch.zeros(S, dtype=torch.int32, device=idx.device)
+    pmean, loss = torch.zeros(S, E, dtype=f64, device=idx.device), torch.zeros(S, dtype=f64, device=idx.device)
+    d = torch.zeros(T, E, dtype=f64, device=idx.device)
+    for j in range(S):
+        t = torch.arange(bounds[j], bounds[j + 1], device=idx.device)
+        t = t[valid[t]]
+        nt = t.numel()
+        if nt == 0:
+            continue
+        kept = idx[t].flatten()
+        c = torch.bincount(kept[kept >= 0], minlength=E)
+        counts[j], ntok[j] = c.int(), nt
+        f = c.to(f64) * E / (k * nt)
+        pmean[j] = p[t].sum(dim=0) / nt
+        loss[j] = (f * pmean[j]).sum()
+        if case["op"] == "bal_bwd":
+            d[t] = s["dloss"][j].to(f64) / nt * p[t] * (f - (p[t] @ f)[:, None])
+    if case["op"] == "bal_fwd":
+        return counts, ntok, pmean, loss
+    if s["w"] is not None:
+        w, dw = s["w"].to(f64), s["dw"].to(f64)
+        kept = w * (dw - (w * dw).sum(dim=1, keepdim=True))
+        for i in range(k):
+            t = torch.nonzero(idx[:, i] >= 0).flatten()
+            d[t, idx[t, i]] += kept[t, i]
+    return d
