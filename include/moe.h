@@ -260,6 +260,105 @@ int moe_layer_forward_ep(const moe_dims *dims, int32_t T, const float *x, const 
                          int32_t *route_counts_opt, int32_t expert_lo, int32_t expert_hi,
                          int32_t with_shared, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The int4 projection with low-rank adapters of many requests beside it, for
+ * an adapted shared expert or any other dense matrix kept as int4 gs64.  (No
+ * counterpart in the source pages, whose engine serves one model unchanged:
+ * an addition of this library.)
+ *
+ * One matrix W [N][K] in the layout of a blob's matrices (N*K/2 packed bytes,
+ * then N*K/64 fp16 scales; gate, up and down of a blob can be passed by their
+ * offsets) and n_adapters pairs A [n][rank][K], B [n][N][rank] of fp16 or
+ * bfloat16, each with a factor scale[a].  Token t uses adapter[t]; any number
+ * outside [0, n_adapters) means no adapter.
+ * Shapes: K % 64 == 0, K <= 8192; N % 8 == 0, N <= 8192; rank % 8 == 0,
+ * 8 <= rank <= 128; n_adapters <= 4096; T <= MOE_LORA_T_MAX.
+ * ------------------------------------------------------------------------ */
+#define MOE_LORA_T_MAX (1 << 19)
+
+enum moe_dtype { MOE_F16 = 0, MOE_BF16 = 1 };
+
+typedef struct moe_lora_dims {
+  int32_t K;          /* inputs */
+  int32_t N;          /* outputs */
+  int32_t n_adapters; /* 0: the projection alone (A, B, scale, adapter may be NULL) */
+  int32_t rank;       /* of every adapter; a smaller one is padded with zeros */
+  int32_t dtype;      /* of A and B: enum moe_dtype */
+} moe_lora_dims;
+
+/* Device workspace of the calls below for up to T_max tokens (256-byte
+ * aligned); with backward != 0 enough for both of them.  0 if the dims are not
+ * accepted.  The backward's is about 4*N*(K + T_max) bytes. */
+size_t moe_lora_workspace_bytes(const moe_lora_dims *dims, int32_t T_max, int32_t backward);
+
+/* out[t] = W^ x^_t + scale_a * B_a (A_a x_t), a = adapter[t]: x^ the Q8_0 codes
+ * of x times their scales, as in the layer; the adapters see x itself.
+ * x [T][K] fp32, out [T][N] fp32, u_opt [T][rank] fp32 or NULL: A_a x_t (0 for
+ * tokens without an adapter), which the backward takes.  x, W, A, B and out
+ * 16-byte aligned; out and u_opt overlap no input.  Block sums are exact
+ * integers; the other sums and the products with A and B are fp32 (22 bits or
+ * more of every factor), in an order that depends on the shapes alone: the
+ * same call gives the same bits.  Capturable in a CUDA graph after one call of
+ * the same dims on the device. */
+int moe_lora_forward(const moe_lora_dims *dims, int32_t T, const float *x, const void *W, const void *A,
+                     const void *B, const float *scale, const int32_t *adapter, float *out, float *u_opt, void *ws,
+                     size_t ws_bytes, void *stream);
+
+/* Gradients of moe_lora_forward for an upstream g [T][N] fp32; W and scale are
+ * constants, and the rounding of x to Q8_0 passes gradients unchanged.  With
+ * v_t = scale_a B_a' g_t and u_t = A_a x_t:
+ *   dx_opt [T][K]       = W^' g_t + A_a' v_t
+ *   dA_opt [n][rank][K] = sum over the adapter's tokens of v_t x_t'
+ *   dB_opt [n][N][rank] = scale_a * sum over them of g_t u_t'
+ * all fp32, overwritten (0 for an adapter without tokens), each may be NULL.
+ * u_opt: the forward's, or NULL (A x is then computed again).  W^' g_t is
+ * computed from 22-bit factors with fp32 sums.  Every pointer but scale,
+ * adapter and u_opt is 16-byte aligned.  The workspace's first word is a
+ * status word as in moe_ws_view (MOE_ERR_TIMEOUT if a bounded wait ran out,
+ * dx is then not valid); the call resets it first. */
+int moe_lora_backward(const moe_lora_dims *dims, int32_t T, const float *g, const float *x, const void *W,
+                      const void *A, const void *B, const float *scale, const int32_t *adapter, const float *u_opt,
+                      float *dx_opt, float *dA_opt, float *dB_opt, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Balance loss of the router, with the per-expert counts behind it, for a
+ * router that is trained: experts that no token selects stay cold, and the
+ * learned pins above live from uneven routes, so both want the measure.  (No
+ * counterpart in the source pages: an addition of this library.)
+ *
+ * Tokens are packed sequences ("segments"): seg_opt [S + 1] int32 on the
+ * device, not decreasing, segment s = tokens [seg[s], seg[s+1]); NULL (S = 1)
+ * means one segment of all T.  valid_opt [T] bytes or NULL: a token with 0 is
+ * counted nowhere; neither is one outside every segment.  logits [T][E] and
+ * idx [T][k] are moe_router_topk's; an idx outside [0, E) is a dropped pair and
+ * is not counted.  S <= MOE_BALANCE_S_MAX.
+ * ------------------------------------------------------------------------ */
+#define MOE_BALANCE_S_MAX 65535
+
+size_t moe_balance_workspace_bytes(const moe_dims *dims, int32_t T_max, int32_t S_max);
+
+/* Per segment, with n its counted tokens and p_t the softmax over all E logits:
+ *   counts [S][E] int32  pairs kept per expert
+ *   ntok   [S] int32     n
+ *   pmean  [S][E] fp32   sum_t p_t / n               (0 if n = 0)
+ *   loss   [S] fp32      sum_e counts_e E / (k n) * pmean_e   (0 if n = 0)
+ * loss is 1 for even routes and probabilities.  A row whose logits are all -inf
+ * has p = 0.  Deterministic. */
+int moe_balance_forward(const moe_dims *dims, int32_t T, int32_t S, const int32_t *seg_opt, const float *logits,
+                        const int32_t *idx, const uint8_t *valid_opt, int32_t *counts, int32_t *ntok, float *pmean,
+                        float *loss, void *ws, size_t ws_bytes, void *stream);
+
+/* dlogits [T][E] (every row written) for upstream gradients dloss [S] of the
+ * losses and, if given, dw_opt [T][k] of the kept weights w_opt [T][k]
+ * (moe_router_topk's softmax over the kept logits); counts are constants:
+ *   dlogits[t][e] = dloss_s / n * p_e (f_e - sum_j f_j p_j),  f = counts E / (k n)
+ *                 + sum over the slots i with idx[t][i] = e of w_i (dw_i - sum_j w_j dw_j).
+ * The first part is 0 for tokens that are not counted, the second is not.
+ * counts and ntok are the forward's; dlogits may be logits itself. */
+int moe_balance_backward(const moe_dims *dims, int32_t T, int32_t S, const int32_t *seg_opt, const float *logits,
+                         const int32_t *idx, const uint8_t *valid_opt, const int32_t *counts, const int32_t *ntok,
+                         const float *dloss, const float *w_opt, const float *dw_opt, float *dlogits, void *stream);
+
 /* The layer in two halves, for callers that must place the experts between
  * routing and the FFN (the tiered cache below):
  *   moe_layer_route:   Q8_0 of x, router + top-k + softmax, batch union into ws

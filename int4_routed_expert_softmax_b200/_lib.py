@@ -30,6 +30,10 @@ class MoeWsView(ctypes.Structure):
         "pair_tok", "hq", "hd")] + [("T_max", ctypes.c_int32)]
 
 
+class MoeLoraDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("K", "N", "n_adapters", "rank", "dtype")]
+
+
 class MoeError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn} failed: {status} ({status_string(status)})")
@@ -47,7 +51,7 @@ def lib() -> ctypes.CDLL:
                                "python -m int4_routed_expert_softmax_b200.build")
         L = ctypes.CDLL(LIB_PATH)
         P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-        D = ctypes.POINTER(MoeDims)
+        D, LD = ctypes.POINTER(MoeDims), ctypes.POINTER(MoeLoraDims)
         sig = {
             "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "moe_check_dims": (ctypes.c_int, [D]),
@@ -68,6 +72,12 @@ def lib() -> ctypes.CDLL:
             "moe_layer_forward_host": (ctypes.c_int, [D, i32, P, P, P, P, P, sz, P, i32, P]),
             "moe_layer_forward_static": (ctypes.c_int, [D, i32, P, P, P, P, P, i32, P]),
             "moe_layer_forward_ep": (ctypes.c_int, [D, i32, P, P, P, P, P, sz, P, i32, i32, i32, P]),
+            "moe_lora_workspace_bytes": (sz, [LD, i32, i32]),
+            "moe_lora_forward": (ctypes.c_int, [LD, i32] + [P] * 9 + [sz, P]),
+            "moe_lora_backward": (ctypes.c_int, [LD, i32] + [P] * 12 + [sz, P]),
+            "moe_balance_workspace_bytes": (sz, [D, i32, i32]),
+            "moe_balance_forward": (ctypes.c_int, [D, i32, i32] + [P] * 9 + [sz, P]),
+            "moe_balance_backward": (ctypes.c_int, [D, i32, i32] + [P] * 11),
             "moe_layer_forward_mxfp4": (ctypes.c_int, [D, i32, P, P, P, P, P, sz, P, P]),
         }
         for name, (res, args) in sig.items():
@@ -277,7 +287,132 @@ def moe_workspace_view(d: MoeDims, T: int, ws: torch.Tensor) -> MoeWsView:
     return v
 
 
+# ----------------------------------------------------------------- adapters and balance
+_LORA_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def lora(K: int, N: int, n_adapters: int, rank: int, dtype=torch.bfloat16) -> MoeLoraDims:
+    """Dims of an int4 projection [N][K] with n_adapters low-rank adapters of `dtype`."""
+    if dtype not in _LORA_DTYPES:
+        raise ValueError(f"adapters must be float16 or bfloat16, got {dtype}")
+    return MoeLoraDims(K, N, n_adapters, rank, _LORA_DTYPES[dtype])
+
+
+def moe_lora_workspace_bytes(p: MoeLoraDims, T_max: int, backward: bool = False) -> int:
+    return int(lib().moe_lora_workspace_bytes(ctypes.byref(p), T_max, 1 if backward else 0))
+
+
+def _lora_args(p: MoeLoraDims, T: int, W, A, B, scale, adapter):
+    N, K, n, r = p.N, p.K, p.n_adapters, p.rank
+    dt = torch.bfloat16 if p.dtype == 1 else torch.float16
+    none = n == 0
+    _arg(W, "W", torch.uint8, N * K // 2 + N * K // 32)
+    _arg(A, "A", dt, n * r * K, optional=none)
+    _arg(B, "B", dt, n * N * r, optional=none)
+    _arg(scale, "scale", torch.float32, n, optional=none)
+    _arg(adapter, "adapter", torch.int32, T, optional=none)
+
+
+def moe_lora_forward(p: MoeLoraDims, x, W, A, B, scale, adapter, out, ws, u=None, stream=None):
+    """out[t] = W^ Q8_0(x_t) + scale_a B_a (A_a x_t), a = adapter[t] (none outside [0, n_adapters)).
+    W: uint8, one int4 gs64 matrix (packed bytes, then scales); A [n][rank][K], B [n][N][rank];
+    u [T][rank] (optional): A_a x_t, for the backward."""
+    T = _rows(x, "x", p.K)
+    _lora_args(p, T, W, A, B, scale, adapter)
+    _arg(out, "out", torch.float32, T * p.N)
+    _arg(u, "u", torch.float32, T * p.rank, optional=True)
+    _arg(ws, "ws", torch.uint8)
+    _check("moe_lora_forward", lib().moe_lora_forward(
+        ctypes.byref(p), T, _ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(scale), _ptr(adapter), _ptr(out), _ptr(u),
+        _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_lora_backward(p: MoeLoraDims, g, x, W, A, B, scale, adapter, ws, u=None, dx=None, dA=None, dB=None,
+                      stream=None):
+    """Gradients of moe_lora_forward for g [T][N]: dx [T][K], dA [n][rank][K], dB [n][N][rank], all float32,
+    each optional.  u: the forward's A x (computed again without it)."""
+    T = _rows(x, "x", p.K)
+    if _rows(g, "g", p.N) != T:
+        raise ValueError(f"g has {g.shape[0]} rows, x has {T}")
+    _lora_args(p, T, W, A, B, scale, adapter)
+    _arg(u, "u", torch.float32, T * p.rank, optional=True)
+    _arg(dx, "dx", torch.float32, T * p.K, optional=True)
+    _arg(dA, "dA", torch.float32, p.n_adapters * p.rank * p.K, optional=True)
+    _arg(dB, "dB", torch.float32, p.n_adapters * p.rank * p.N, optional=True)
+    _arg(ws, "ws", torch.uint8)
+    _check("moe_lora_backward", lib().moe_lora_backward(
+        ctypes.byref(p), T, _ptr(g), _ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(scale), _ptr(adapter), _ptr(u),
+        _ptr(dx), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_balance_workspace_bytes(d: MoeDims, T_max: int, S_max: int = 1) -> int:
+    return int(lib().moe_balance_workspace_bytes(ctypes.byref(d), T_max, S_max))
+
+
+def _balance_args(d: MoeDims, logits, idx, counts, ntok, seg, valid):
+    T = _rows(logits, "logits", d.E)
+    S = 1
+    if seg is not None:
+        _arg(seg, "seg", torch.int32, 2)
+        S = seg.numel() - 1
+    _arg(idx, "idx", torch.int32, T * d.k)
+    _arg(valid, "valid", torch.uint8, T, optional=True)
+    _arg(counts, "counts", torch.int32, S * d.E)
+    _arg(ntok, "ntok", torch.int32, S)
+    return T, S
+
+
+def moe_balance_forward(d: MoeDims, logits, idx, counts, ntok, pmean, loss, ws, seg=None, valid=None, stream=None):
+    """Balance loss per segment of packed tokens: counts [S][E] and ntok [S] int32, pmean [S][E] and
+    loss [S] float32 from logits [T][E] and idx [T][k].  seg: [S+1] int32 token offsets (one segment
+    without it); valid: [T] uint8, 0 for tokens that are not counted."""
+    T, S = _balance_args(d, logits, idx, counts, ntok, seg, valid)
+    _arg(pmean, "pmean", torch.float32, S * d.E)
+    _arg(loss, "loss", torch.float32, S)
+    _arg(ws, "ws", torch.uint8)
+    _check("moe_balance_forward", lib().moe_balance_forward(
+        ctypes.byref(d), T, S, _ptr(seg), _ptr(logits), _ptr(idx), _ptr(valid), _ptr(counts), _ptr(ntok),
+        _ptr(pmean), _ptr(loss), _ptr(ws), ws.numel(), _stream(stream)))
+
+
+def moe_balance_backward(d: MoeDims, logits, idx, counts, ntok, dloss, dlogits, seg=None, valid=None, w=None,
+                         dw=None, stream=None):
+    """dlogits [T][E] for dloss [S] and, with w and dw [T][k], for the gradient of the kept weights."""
+    T, S = _balance_args(d, logits, idx, counts, ntok, seg, valid)
+    _arg(dloss, "dloss", torch.float32, S)
+    _arg(dlogits, "dlogits", torch.float32, T * d.E)
+    if (w is None) != (dw is None):
+        raise ValueError("w and dw come together")
+    _arg(w, "w", torch.float32, T * d.k, optional=True)
+    _arg(dw, "dw", torch.float32, T * d.k, optional=True)
+    _check("moe_balance_backward", lib().moe_balance_backward(
+        ctypes.byref(d), T, S, _ptr(seg), _ptr(logits), _ptr(idx), _ptr(valid), _ptr(counts), _ptr(ntok),
+        _ptr(dloss), _ptr(w), _ptr(dw), _ptr(dlogits), _stream(stream)))
+
+
 # ----------------------------------------------------------------- helpers
+def _alloc(n: int, device) -> torch.Tensor:
+    ws = torch.empty(n + 256, dtype=torch.uint8, device=device)
+    off = (-ws.data_ptr()) % 256
+    return ws[off:off + n]
+
+
+def alloc_lora_workspace(p: MoeLoraDims, T_max: int, device="cuda", backward: bool = False) -> torch.Tensor:
+    """Device workspace of moe_lora_forward (and, if `backward`, of moe_lora_backward) for up to T_max tokens."""
+    n = moe_lora_workspace_bytes(p, T_max, backward)
+    if n == 0:
+        raise MoeError("moe_lora_workspace_bytes", -2)
+    return _alloc(n, device)
+
+
+def alloc_balance_workspace(d: MoeDims, T_max: int, S_max: int = 1, device="cuda") -> torch.Tensor:
+    """Device workspace of moe_balance_forward for up to T_max tokens in S_max segments."""
+    n = moe_balance_workspace_bytes(d, T_max, S_max)
+    if n == 0:
+        raise MoeError("moe_balance_workspace_bytes", -2)
+    return _alloc(n, device)
+
+
 def alloc_workspace(d: MoeDims, T_max: int, device="cuda", path: int = MOE_PATH_AUTO) -> torch.Tensor:
     """Device workspace for batches of up to T_max tokens on `path` (256-byte aligned)."""
     n = moe_workspace_bytes_path(d, T_max, path)

@@ -1,0 +1,268 @@
+// moe_adapt.cpp -- C ABI of the adapter projection and of the balance loss
+// (declared in include/moe.h): argument checks, workspace layout, launches.
+#include <cstdio>
+
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+int cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  std::fprintf(stderr, "libmoe: CUDA error %d (%s)\n", (int)e, cudaGetErrorString(e));
+  return MOE_ERR_CUDA;
+}
+
+template <typename T>
+T *at(void *ws, size_t off) {
+  return reinterpret_cast<T *>(static_cast<unsigned char *>(ws) + off);
+}
+
+int check_lora(const moe_lora_dims *p, int32_t T) {
+  if (p == nullptr || T < 0) return MOE_ERR_BAD_ARG;
+  if (p->dtype != MOE_F16 && p->dtype != MOE_BF16) return MOE_ERR_BAD_ARG;
+  if (p->K < 64 || p->K % 64 != 0 || p->K > 8192 || p->N < 8 || p->N % 8 != 0 || p->N > 8192 || p->n_adapters < 0 ||
+      p->n_adapters > kLoraMaxAdapters || p->rank < 8 || p->rank % 8 != 0 || p->rank > kLoraMaxRank ||
+      T > MOE_LORA_T_MAX)
+    return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+struct LoraLayout {
+  size_t status, perm, off, tile, us;     // both calls
+  size_t xq, xs, upart;                   // forward
+  size_t v, wt, gs, gexp, wexp;           // backward
+  size_t total;
+};
+
+LoraLayout lora_layout(const moe_lora_dims &p, int T, bool backward) {
+  LoraLayout L{};
+  size_t o = 0;
+  auto seg = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + (bytes ? bytes : 1), 256);
+    return at;
+  };
+  const size_t Tp = align_up((size_t)(T < 1 ? 1 : T), kLoraTile), K = p.K, N = p.N, r = p.rank, n = p.n_adapters;
+  L.status = seg(16);
+  L.perm = seg(Tp * 4);
+  L.off = seg((n + 2) * 4);
+  L.tile = seg((n + 2) * 4);
+  L.us = seg(Tp * r * 4);
+  if (backward) {
+    const size_t Np = align_up(N, 64);
+    L.v = seg(Tp * r * 4);
+    L.wt = seg(K * 2 * Np * 2);
+    L.gs = seg(Tp * 2 * Np * 2);
+    L.gexp = seg(Tp * 4);
+    L.wexp = seg(2 * N * 4);
+  } else {
+    L.xq = seg(Tp * K);
+    L.xs = seg(Tp / 2 * (K / 64) * 32);
+    L.upart = seg((K + kLoraSlice - 1) / kLoraSlice * (size_t)kLoraSmallT * r * 4);
+  }
+  L.total = o;
+  return L;
+}
+
+LoraArgs lora_args(const moe_lora_dims &p, int T, const float *x, const void *W, const void *A, const void *B,
+                   const float *scale, const int32_t *adapter, void *ws, const LoraLayout &L) {
+  LoraArgs a{};
+  a.K = p.K;
+  a.N = p.N;
+  a.n = p.n_adapters;
+  a.r = p.rank;
+  a.T = T;
+  a.bf16 = p.dtype == MOE_BF16;
+  a.x = x;
+  a.W = static_cast<const unsigned char *>(W);
+  a.A = A;
+  a.B = B;
+  a.scale = scale;
+  a.adapter = adapter;
+  a.perm = at<int32_t>(ws, L.perm);
+  a.off = at<int32_t>(ws, L.off);
+  a.tile = at<int32_t>(ws, L.tile);
+  a.us = at<float>(ws, L.us);
+  a.status = at<int32_t>(ws, L.status);
+  a.wait_limit = wait_limit_cycles();
+  return a;
+}
+
+// Not the plan's own grid, which may fall by a few CTAs as T grows: a
+// workspace for T_max tokens serves every smaller batch.
+size_t balance_slots(int T, int S, int sms) {
+  const int64_t most = ((int64_t)T + kBalanceChunkMin - 1) / kBalanceChunkMin;
+  return (size_t)(most < kBalanceCtas * sms ? most : kBalanceCtas * sms) + (size_t)S + 1;
+}
+
+struct BalanceLayout {
+  size_t part_p, part_c, part_n, part_l, ticket, total;
+};
+
+BalanceLayout balance_layout(const moe_dims &d, int T, int S, int sms) {
+  BalanceLayout L{};
+  size_t o = 0;
+  auto seg = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + (bytes ? bytes : 1), 256);
+    return at;
+  };
+  const size_t slots = balance_slots(T, S, sms);
+  L.part_p = seg(slots * d.E * 4);
+  L.part_c = seg(slots * d.E * 4);
+  L.part_n = seg(slots * 4);
+  L.part_l = seg((size_t)S * ((d.E + 31) / 32) * 4);
+  L.ticket = seg((size_t)S * 4);
+  L.total = o;
+  return L;
+}
+
+int check_balance(const moe_dims *dims, int32_t T, int32_t S, const int32_t *seg_opt) {
+  const int rc = moe_check_dims(dims);
+  if (rc != MOE_OK) return rc;
+  if (T < 0 || S < 1 || (S > 1 && seg_opt == nullptr)) return MOE_ERR_BAD_ARG;
+  if (S > MOE_BALANCE_S_MAX) return MOE_ERR_SHAPE;
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_lora_workspace_bytes(const moe_lora_dims *dims, int32_t T_max, int32_t backward) {
+  if (check_lora(dims, T_max) != MOE_OK) return 0;
+  const size_t f = lora_layout(*dims, T_max, false).total;
+  if (!backward) return f;
+  const size_t b = lora_layout(*dims, T_max, true).total;
+  return f > b ? f : b;
+}
+
+int moe_lora_forward(const moe_lora_dims *dims, int32_t T, const float *x, const void *W, const void *A, const void *B,
+                     const float *scale, const int32_t *adapter, float *out, float *u_opt, void *ws, size_t ws_bytes,
+                     void *stream) {
+  int rc = check_lora(dims, T);
+  if (rc != MOE_OK) return rc;
+  if (T == 0) return MOE_OK;
+  if (!x || !W || !out || !ws || (dims->n_adapters > 0 && (!A || !B || !scale || !adapter))) return MOE_ERR_BAD_ARG;
+  if (!aligned(x, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(out, 16))
+    return MOE_ERR_BAD_ARG;
+  if (!aligned(ws, 256)) return MOE_ERR_WORKSPACE;
+  const LoraLayout L = lora_layout(*dims, T, false);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  LoraArgs a = lora_args(*dims, T, x, W, A, B, scale, adapter, ws, L);
+  a.out = out;
+  a.u = u_opt;
+  a.xq = at<int8_t>(ws, L.xq);
+  a.xs = at<float>(ws, L.xs);
+  a.upart = at<float>(ws, L.upart);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T <= kLoraSmallT) return cuda_status(launch_lora_small(a, s));
+  const int sms = moe_device_sms();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  return cuda_status(launch_lora_large(a, sms, s));
+}
+
+int moe_lora_backward(const moe_lora_dims *dims, int32_t T, const float *g, const float *x, const void *W,
+                      const void *A, const void *B, const float *scale, const int32_t *adapter, const float *u_opt,
+                      float *dx_opt, float *dA_opt, float *dB_opt, void *ws, size_t ws_bytes, void *stream) {
+  int rc = check_lora(dims, T);
+  if (rc != MOE_OK) return rc;
+  if (!ws || (dims->n_adapters > 0 && (!A || !B || !scale))) return MOE_ERR_BAD_ARG;
+  if (T > 0 && (!g || !x || !W || (dims->n_adapters > 0 && !adapter))) return MOE_ERR_BAD_ARG;
+  if (!aligned(g, 16) || !aligned(x, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) ||
+      !aligned(dx_opt, 16) || !aligned(dA_opt, 16) || !aligned(dB_opt, 16))
+    return MOE_ERR_BAD_ARG;
+  if (!aligned(ws, 256)) return MOE_ERR_WORKSPACE;
+  const LoraLayout L = lora_layout(*dims, T, true);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  LoraArgs a = lora_args(*dims, T, x, W, A, B, scale, adapter, ws, L);
+  a.u = const_cast<float *>(u_opt);
+  a.g = g;
+  a.dx = dx_opt;
+  a.dA = dA_opt;
+  a.dB = dB_opt;
+  a.v = at<float>(ws, L.v);
+  a.wt = at<void>(ws, L.wt);
+  a.gs = at<void>(ws, L.gs);
+  a.gexp = at<float>(ws, L.gexp);
+  a.wexp = at<float>(ws, L.wexp);
+  return cuda_status(launch_lora_bwd(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_balance_workspace_bytes(const moe_dims *dims, int32_t T_max, int32_t S_max) {
+  if (moe_check_dims(dims) != MOE_OK || T_max < 0 || S_max < 1 || S_max > MOE_BALANCE_S_MAX) return 0;
+  const int sms = moe_device_sms();
+  return balance_layout(*dims, T_max, S_max, sms > 0 ? sms : 148).total;
+}
+
+int moe_balance_forward(const moe_dims *dims, int32_t T, int32_t S, const int32_t *seg_opt, const float *logits,
+                        const int32_t *idx, const uint8_t *valid_opt, int32_t *counts, int32_t *ntok, float *pmean,
+                        float *loss, void *ws, size_t ws_bytes, void *stream) {
+  const int rc = check_balance(dims, T, S, seg_opt);
+  if (rc != MOE_OK) return rc;
+  if ((T > 0 && (!logits || !idx)) || !counts || !ntok || !pmean || !loss || !ws) return MOE_ERR_BAD_ARG;
+  if (!aligned(logits, 4)) return MOE_ERR_BAD_ARG;
+  if (!aligned(ws, 256)) return MOE_ERR_WORKSPACE;
+  const int sms = moe_device_sms();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  const BalanceLayout L = balance_layout(*dims, T, S, sms);
+  if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  const BalancePlan plan = balance_plan(T, sms);
+  BalanceArgs a{};
+  a.T = T;
+  a.S = S;
+  a.E = dims->E;
+  a.k = dims->k;
+  a.chunk = plan.chunk;
+  a.seg = seg_opt;
+  a.logits = logits;
+  a.idx = idx;
+  a.valid = valid_opt;
+  a.counts = counts;
+  a.ntok = ntok;
+  a.pmean = pmean;
+  a.loss = loss;
+  a.part_p = at<float>(ws, L.part_p);
+  a.part_c = at<int32_t>(ws, L.part_c);
+  a.part_n = at<int32_t>(ws, L.part_n);
+  a.part_l = at<float>(ws, L.part_l);
+  a.ticket = at<unsigned int>(ws, L.ticket);
+  return cuda_status(launch_balance_fwd(a, plan.grid, static_cast<cudaStream_t>(stream)));
+}
+
+int moe_balance_backward(const moe_dims *dims, int32_t T, int32_t S, const int32_t *seg_opt, const float *logits,
+                         const int32_t *idx, const uint8_t *valid_opt, const int32_t *counts, const int32_t *ntok,
+                         const float *dloss, const float *w_opt, const float *dw_opt, float *dlogits, void *stream) {
+  const int rc = check_balance(dims, T, S, seg_opt);
+  if (rc != MOE_OK) return rc;
+  if (T == 0) return MOE_OK;
+  if (!logits || !counts || !ntok || !dloss || !dlogits) return MOE_ERR_BAD_ARG;
+  if ((w_opt == nullptr) != (dw_opt == nullptr) || (dw_opt != nullptr && !idx)) return MOE_ERR_BAD_ARG;
+  if (!aligned(logits, 4) || !aligned(dlogits, 4)) return MOE_ERR_BAD_ARG;
+  const int sms = moe_device_sms();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  BalanceArgs a{};
+  a.T = T;
+  a.S = S;
+  a.E = dims->E;
+  a.k = dims->k;
+  a.seg = seg_opt;
+  a.logits = logits;
+  a.idx = idx;
+  a.valid = valid_opt;
+  a.counts = const_cast<int32_t *>(counts);
+  a.ntok = const_cast<int32_t *>(ntok);
+  a.dloss = dloss;
+  a.w = w_opt;
+  a.dw = dw_opt;
+  a.dlogits = dlogits;
+  return cuda_status(launch_balance_bwd(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

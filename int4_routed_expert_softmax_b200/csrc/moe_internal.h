@@ -61,6 +61,10 @@ enum Detail : int32_t {
   kDetFuSlot = 46,
   kDetFuAlign = 47,
   kDetFuReady = 48,
+  kDetLoraFull = 50,
+  kDetLoraEmpty = 51,
+  kDetLoraAcc = 52,
+  kDetLoraDrain = 53,
 };
 
 // The wait limit kernels launched now take for their work waits (set by
@@ -286,6 +290,70 @@ struct CombineArgs {
   float *out;
   unsigned long long *prof;  // profiling record or null (phase 2 end)
 };
+
+// Balance loss of the router (moe_balance.cu).
+struct BalanceArgs {
+  int T, S, E, k;
+  int chunk;               // consecutive tokens per CTA (forward) or per warp (backward)
+  const int32_t *seg;      // [S + 1] token offsets or null (one segment: every token)
+  const float *logits;     // [T][E]
+  const int32_t *idx;      // [T][k], entries outside [0, E) are dropped pairs
+  const uint8_t *valid;    // [T] or null
+  int32_t *counts, *ntok;  // [S][E], [S]: written by the forward, read by the backward
+  float *pmean, *loss;     // [S][E], [S]
+  float *part_p, *part_l;  // forward of more than one CTA: sums per (CTA, segment) slot, loss shares
+  int32_t *part_c, *part_n;
+  unsigned int *ticket;    // [S]
+  const float *dloss, *w, *dw;  // backward: [S], [T][k] or null, [T][k] or null
+  float *dlogits;          // [T][E]
+};
+constexpr int kBalanceChunkMin = 32;  // tokens a CTA of the forward takes at least,
+constexpr int kBalanceCtas = 2;       // and CTAs per SM at most
+// CTAs and tokens per CTA of the forward.
+struct BalancePlan {
+  int grid, chunk;
+};
+BalancePlan balance_plan(int T, int sms);
+cudaError_t launch_balance_fwd(const BalanceArgs &a, int grid, cudaStream_t s);
+cudaError_t launch_balance_bwd(const BalanceArgs &a, int sms, cudaStream_t s);
+
+// int4 projection with low-rank adapters (moe_lora.cu, moe_lora_bwd.cu).
+constexpr int kLoraSmallT = 32;      // the largest batch the token-order kernels take
+constexpr int kLoraSlice = 512;      // inputs per CTA of their first kernel
+constexpr int kLoraMaxRank = 128;
+constexpr int kLoraMaxAdapters = 4096;
+constexpr int kLoraTile = 128;       // sorted positions are padded to this many
+constexpr int kLoraSeg = 16;         // tokens of one adapter per tile of the per-adapter kernels
+
+struct LoraArgs {
+  int K, N, n, r, T;
+  int bf16;                 // A and B hold bfloat16 (else fp16)
+  const float *x;           // [T][K]
+  const unsigned char *W;   // int4 gs64 [N][K]
+  const void *A, *B;        // [n][r][K], [n][N][r]
+  const float *scale;       // [n]
+  const int32_t *adapter;   // [T]
+  float *out, *u;           // [T][N], [T][r] or null
+  // workspace; rows by position: the token itself in token order, else its place among the
+  // tokens sorted by adapter
+  int8_t *xq;               // [Tp][K] Q8_0 codes
+  float *xs;                // [Tp / 2][K / 64][8] scales and code sums of two positions (moe_lora.cu)
+  float *upart;             // [slices][T][r] partial A x (token order)
+  float *us;                // [Tp][r] scale * A x by sorted position
+  int32_t *perm, *off, *tile;  // sorted order: token of each position, first position and tile per adapter
+  // backward
+  const float *g;           // [T][N]
+  float *dx, *dA, *dB;      // [T][K], [n][r][K], [n][N][r], each may be null
+  float *v;                 // [Tp][r] scale * B' g by sorted position
+  void *wt, *gs;            // fp16 hi / lo of W^ transposed and of g (moe_lora_bwd.cu)
+  float *gexp;              // [T] undoes the power of two of a row of gs
+  float *wexp;              // [2][N] powers of two of W's rows, and their inverses
+  int32_t *status;
+  long long wait_limit;
+};
+cudaError_t launch_lora_small(const LoraArgs &a, cudaStream_t s);
+cudaError_t launch_lora_large(const LoraArgs &a, int sms, cudaStream_t s);
+cudaError_t launch_lora_bwd(const LoraArgs &a, cudaStream_t s);
 
 // Offsets of the union mailbox (mapped pinned host memory the routing kernel
 // writes for the tiered cache): sequence number, union size, union.

@@ -1,0 +1,156 @@
+// moe_lora.cuh -- device helpers of the adapter kernels (moe_lora.cu,
+// moe_lora_bwd.cu): warp-level matrix products and the packed fp32 arithmetic.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "moe_device.cuh"
+
+namespace moe {
+
+// ------------------------------------------------------------------ adapters' values
+template <bool BF16>
+__device__ __forceinline__ float half_value(uint16_t h) {
+  return BF16 ? __uint_as_float((uint32_t)h << 16) : __half2float(__ushort_as_half(h));
+}
+// The two values of a 32-bit word, the lower-indexed one first.
+template <bool BF16>
+__device__ __forceinline__ float2 half2_values(uint32_t w) {
+  if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// ------------------------------------------------------------------ tf32 products
+// A value as tf32 hi + lo: 11 significant bits each, rounded, so that what is
+// lost is at most 2^-22 of the value.  fp16 and bfloat16 values are exact in
+// tf32 (11 and 8 bits), so a product with an adapter's value needs two MMAs.
+__device__ __forceinline__ uint32_t to_tf32(float v) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(v));
+  return r;
+}
+struct Tf32Pair {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Tf32Pair split_tf32(float v) {
+  Tf32Pair p;
+  p.hi = to_tf32(v);
+  // an infinite (or NaN) value has no rest: inf - inf would make it NaN
+  const float rest = v - __uint_as_float(p.hi);
+  p.lo = fabsf(v) <= 3.0e38f ? to_tf32(rest) : 0u;
+  return p;
+}
+// D[16][8] += A[16][8] B[8][8]; lane = 4 g + q: a = A(g, q), A(g + 8, q),
+// A(g, q + 4), A(g + 8, q + 4); b = B(q, g), B(q + 4, g); d = D(g, 2q),
+// D(g, 2q + 1), D(g + 8, 2q), D(g + 8, 2q + 1).
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// ------------------------------------------------------------------ integer products
+// Block sums: D[16][8] = A[16][32] (unsigned bytes) B[32][8] (signed bytes) + C,
+// C the same for every row.  Lane 4 g + q holds bytes 4q .. 4q + 3 and
+// 16 + 4q .. of rows g (a0, a2) and g + 8 (a1, a3) and of column g (b0, b1).
+__device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, int c0, int c1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0), "r"(c1));
+}
+// The sums leave the MMA as floats: started from the bit pattern of
+// 1.5 * 2^23, an integer of magnitude below 2^22 added to it is the float
+// 1.5 * 2^23 + sum, exactly.
+constexpr int kMagicBits = 0x4B400000;
+constexpr float kMagic = 12582912.0f;
+
+// ------------------------------------------------------------------ packed fp32
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pack2(float a, float b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 pack2i(int a, int b) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The adapter of token t, or n (none) for any number outside [0, n).
+__device__ __forceinline__ int adapter_of(const LoraArgs &a, int t) {
+  if (a.n == 0) return 0;
+  const int id = a.adapter[t];
+  return id >= 0 && id < a.n ? id : a.n;
+}
+
+// Adapter whose sorted positions hold p (n for the tokens without one).
+__device__ __forceinline__ int adapter_at(const int32_t *off, int n, int p) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid + 1] > p) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Launch with programmatic stream serialisation: the kernel may start before
+// the previous one of the stream ends and waits for it with pdl_wait.
+template <typename... P, typename... A>
+inline cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// moe_lora.cu, used by the backward too
+cudaError_t launch_lora_sort(const LoraArgs &a, cudaStream_t s);
+// dst[p][j] = scale_a sum_k src[token][k] M_a(j, k) by sorted position; M_a(j, k) =
+// A_a[j][k], or B_a[k][j] if `transposed`.  user (or null): the unscaled sums
+// by token, 0 for tokens without an adapter.
+cudaError_t launch_lora_shrink(const LoraArgs &a, const float *src, int L, const void *M, bool transposed, float *dst,
+                               float *user, cudaStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,461 @@
+// moe_lora_bwd.cu -- backward of the int4 projection with low-rank adapters.
+// For an upstream g, with v_t = scale_a B_a' g_t and u_t = A_a x_t,
+//
+//   dx_t = W^' g_t + A_a' v_t,
+//   dA_a = sum over the adapter's tokens of v_t x_t',
+//   dB_a = scale_a sum over them of g_t u_t'
+//
+// (W^ is frozen; the Q8_0 rounding of x passes gradients unchanged).
+//
+//   k_lora_sort    : tokens by adapter (moe_lora.cu);
+//   k_lora_shrink  : v, and u where the caller kept none (moe_lora.cu);
+//   k_lora_outer   : dA and dB, a tile of the matrix per CTA, its warps
+//                    splitting the adapter's tokens (tf32 hi + lo, three MMAs);
+//   k_lora_wexp, k_lora_wt, k_lora_gsplit: fp16 hi + lo of W^' and of g;
+//   k_lora_dx      : W^' g on the fifth-generation tensor cores;
+//   k_lora_expand  : adds A_a' v.
+//
+// The base product g W^ has no integer form: g is fp32.  Both operands enter
+// as fp16 hi + lo (22 bits) and three tcgen05.mma per product (hi hi, hi lo,
+// lo hi; lo lo is below 2^-22 of the product).  fp16's exponents do not reach
+// over a gradient's, so every row of W is scaled by a power of two that brings
+// its largest value near 2^15 (its inverse goes to g's column), and then every
+// row of g by one of its own, undone in the epilogue.  An int4 weight times
+// its fp16 scale has at most 15 significant bits, so W^' is exact in hi + lo as
+// long as a group's scale is within 2^-15 of its row's largest.
+#include "moe_lora.cuh"
+#include "moe_umma.cuh"
+
+namespace moe {
+namespace {
+
+// 2^e with e such that |m| 2^e lies in [2^14, 2^15) (1 for 0 and for what is
+// not finite, whose products are not finite at any scale).
+__device__ __forceinline__ float pow2_to_15(float m) {
+  if (!(m > 0.0f) || !(m <= 3.0e38f)) return 1.0f;
+  const int e = (int)(__float_as_uint(m) >> 23) - 127;  // -127 for denormals, which stay small
+  const int k = min(max(14 - e, -126), 126);
+  return __uint_as_float((uint32_t)(k + 127) << 23);
+}
+
+__device__ __forceinline__ void split_f16(float v, __half &hi, __half &lo) {
+  hi = __float2half_rn(v);
+  lo = __float2half_rn(v - __half2float(hi));
+}
+
+// ===========================================================================
+// dA, dB: D[j][l] = sum over the adapter's tokens of left[p][j] right[t][l].
+// left: fp32 rows of r by position (or by token, `left_by_token`, then times
+// scale_a); right: fp32 rows of L by token.  A warp holds 32 columns l (a lane
+// reads four consecutive ones for four MMA tiles) by up to 64 rows j, and
+// takes every fourth step of 8 tokens; the four warps of a column block are
+// joined in shared memory in a fixed order.  out is [n][r][L], or [n][L][r]
+// if `l_major`.
+// ===========================================================================
+constexpr int kOuterL = 64;  // columns per CTA (two blocks of 32)
+constexpr int kOuterJ = 64;  // rows per CTA
+
+template <int RM>
+__global__ void __launch_bounds__(256) k_lora_outer(const LoraArgs a, const float *left, int left_by_token,
+                                                    const float *right, int L, float *out, int l_major) {
+  __shared__ float red[3][2][32][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int id = blockIdx.y, r = a.r;
+  const int lb = blockIdx.x * kOuterL + (warp & 1) * 32, j0 = blockIdx.z * kOuterJ, tw = warp >> 1;
+  const int p0 = a.off[id], p1 = a.off[id + 1];
+  const int l = lb + 4 * g;
+  const bool in = l < L;  // L % 8 == 0
+  const float sc = left_by_token ? a.scale[id] : 1.0f;
+  float acc[RM][4][4];
+#pragma unroll
+  for (int m = 0; m < RM; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[m][i][c] = 0.0f;
+  for (int p = p0 + 8 * tw; p < p1; p += 32) {
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int pa = p + q, pb = p + q + 4;
+    const bool va = pa < p1, vb = pb < p1;
+    const int ta = va ? a.perm[pa] : 0, tb = vb ? a.perm[pb] : 0;
+    const float4 xa = va && in ? *reinterpret_cast<const float4 *>(right + (size_t)ta * L + l) : zero;
+    const float4 xb = vb && in ? *reinterpret_cast<const float4 *>(right + (size_t)tb * L + l) : zero;
+    const float *la = left + (size_t)(left_by_token ? ta : pa) * r, *lo_ = left + (size_t)(left_by_token ? tb : pb) * r;
+    const float fa[4] = {xa.x, xa.y, xa.z, xa.w}, fb[4] = {xb.x, xb.y, xb.z, xb.w};
+    Tf32Pair ba[4], bb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ba[i] = split_tf32(fa[i]);
+      bb[i] = split_tf32(fb[i]);
+    }
+#pragma unroll
+    for (int m = 0; m < RM; ++m) {
+      const int j = j0 + m * 16 + g;
+      Tf32Pair e[4];
+      e[0] = split_tf32(va && j < r ? sc * la[j] : 0.0f);
+      e[1] = split_tf32(va && j + 8 < r ? sc * la[j + 8] : 0.0f);
+      e[2] = split_tf32(vb && j < r ? sc * lo_[j] : 0.0f);
+      e[3] = split_tf32(vb && j + 8 < r ? sc * lo_[j + 8] : 0.0f);
+      const uint32_t hi[4] = {e[0].hi, e[1].hi, e[2].hi, e[3].hi}, lw[4] = {e[0].lo, e[1].lo, e[2].lo, e[3].lo};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mma_tf32(acc[m][i], hi, ba[i].hi, bb[i].hi);
+        mma_tf32(acc[m][i], hi, ba[i].lo, bb[i].lo);
+        mma_tf32(acc[m][i], lw, ba[i].hi, bb[i].hi);
+      }
+    }
+  }
+  // join the four token shares, 16 rows at a time (a lane's 16 sums as a row of red)
+#pragma unroll
+  for (int m = 0; m < RM; ++m) {
+    __syncthreads();
+    if (tw > 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) red[tw - 1][warp & 1][lane][4 * i + c] = acc[m][i][c];
+    }
+    __syncthreads();
+    if (tw == 0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          for (int w = 0; w < 3; ++w) acc[m][i][c] += red[w][warp & 1][lane][4 * i + c];
+      // acc[m][i]: rows g, g + 8, columns 4 * 2q + i and 4 * (2q + 1) + i of the block
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = j0 + m * 16 + g + 8 * h;
+        if (j >= r || lb + 8 * q >= L) continue;
+        if (l_major) {
+          float *o = out + ((size_t)id * L + lb + 8 * q) * r + j;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            o[(size_t)i * r] = acc[m][i][2 * h];
+            o[(size_t)(4 + i) * r] = acc[m][i][2 * h + 1];
+          }
+        } else {
+          float4 *o = reinterpret_cast<float4 *>(out + ((size_t)id * r + j) * L + lb + 8 * q);
+          o[0] = make_float4(acc[m][0][2 * h], acc[m][1][2 * h], acc[m][2][2 * h], acc[m][3][2 * h]);
+          o[1] = make_float4(acc[m][0][2 * h + 1], acc[m][1][2 * h + 1], acc[m][2][2 * h + 1], acc[m][3][2 * h + 1]);
+        }
+      }
+    }
+  }
+}
+
+// ===========================================================================
+// operands of the base product
+// ===========================================================================
+// wexp[n] = the power of two of row n of W (from its largest scale), wexp[N + n] its inverse.
+__global__ void __launch_bounds__(256) k_lora_wexp(const LoraArgs a) {
+  const int n = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (n >= a.N) return;
+  const int G = a.K / 64;
+  const __half *sc = reinterpret_cast<const __half *>(a.W + (size_t)a.N * (a.K / 2)) + (size_t)n * G;
+  float m = 0.0f;
+  for (int g = lane; g < G; g += 32) m = fmaxf(m, fabsf(__half2float(sc[g])));
+  m = warp_max(m);
+  if (lane == 0) {
+    const float e = pow2_to_15(8.0f * m);
+    a.wexp[n] = e;
+    // a row of zeros must not set the power of two of g's rows
+    a.wexp[a.N + n] = m == 0.0f ? 0.0f : 1.0f / e;
+  }
+}
+
+// wt [K][2 Np]: per 64 rows of W 64 hi then 64 lo of column k, times wexp[n];
+// a CTA transposes 64 rows by one 64-group.
+__global__ void __launch_bounds__(256) k_lora_wt(const LoraArgs a) {
+  __shared__ __half hi[64][72], lo[64][72];  // [k][n]
+  const int n0 = blockIdx.x * 64, g = blockIdx.y, G = a.K / 64;
+  const int tid = threadIdx.x, n = tid & 63, part = tid >> 6;  // 8 packed bytes each
+  uint2 w = make_uint2(0x88888888u, 0x88888888u);
+  float s = 0.0f;
+  if (n0 + n < a.N) {
+    w = __ldg(reinterpret_cast<const uint2 *>(a.W + (size_t)(n0 + n) * (a.K / 2) + (size_t)g * 32 + part * 8));
+    const __half *sc = reinterpret_cast<const __half *>(a.W + (size_t)a.N * (a.K / 2));
+    s = __half2float(sc[(size_t)(n0 + n) * G + g]) * a.wexp[n0 + n];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t b = ((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 255u;
+    const int k = part * 8 + i;
+    split_f16((float)((int)(b & 15u) - 8) * s, hi[k][n], lo[k][n]);
+    split_f16((float)((int)(b >> 4) - 8) * s, hi[k + 32][n], lo[k + 32][n]);
+  }
+  __syncthreads();
+  const int Np = (a.N + 63) / 64 * 64;
+  __half *wt = static_cast<__half *>(a.wt);
+  for (int i = tid; i < 64 * 16; i += 256) {
+    const int k = i >> 4, c = i & 15;  // 16-byte pieces: 8 of hi, 8 of lo
+    const __half *src = c < 8 ? &hi[k][c * 8] : &lo[k][(c - 8) * 8];
+    *reinterpret_cast<uint4 *>(wt + ((size_t)g * 64 + k) * (2 * (size_t)Np) + (size_t)n0 * 2 + c * 8) =
+        *reinterpret_cast<const uint4 *>(src);
+  }
+}
+
+// gs [T][2 Np]: g's row over wexp, times a power of two of its own; gexp[t] =
+// its inverse.
+__global__ void __launch_bounds__(256) k_lora_gsplit(const LoraArgs a) {
+  __shared__ float wm[8];
+  const int t = blockIdx.x, tid = threadIdx.x;
+  const float *g = a.g + (size_t)t * a.N, *inv = a.wexp + a.N;
+  const int Np = (a.N + 63) / 64 * 64;
+  float m = 0.0f;
+  for (int n = 4 * tid; n < a.N; n += 1024) {
+    const float4 v = *reinterpret_cast<const float4 *>(g + n), e = *reinterpret_cast<const float4 *>(inv + n);
+    m = fmaxf(m, fmaxf(fmaxf(fabsf(v.x * e.x), fabsf(v.y * e.y)), fmaxf(fabsf(v.z * e.z), fabsf(v.w * e.w))));
+  }
+  m = warp_max(m);
+  if ((tid & 31) == 0) wm[tid >> 5] = m;
+  __syncthreads();
+  m = wm[0];
+#pragma unroll
+  for (int w = 1; w < 8; ++w) m = fmaxf(m, wm[w]);
+  const float f = pow2_to_15(m);
+  if (tid == 0) a.gexp[t] = 1.0f / f;
+  __half *row = static_cast<__half *>(a.gs) + (size_t)t * (2 * (size_t)Np);
+  for (int n = 4 * tid; n < Np; n += 1024) {
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n < a.N) {
+      const float4 x = *reinterpret_cast<const float4 *>(g + n), e = *reinterpret_cast<const float4 *>(inv + n);
+      v[0] = x.x * e.x * f, v[1] = x.y * e.y * f, v[2] = x.z * e.z * f, v[3] = x.w * e.w * f;
+    }
+    __half h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_f16(v[i], h[i], l[i]);
+    __half *o = row + (n >> 6) * 128 + (n & 63);
+    *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(h);
+    *reinterpret_cast<uint2 *>(o + 64) = *reinterpret_cast<const uint2 *>(l);
+  }
+}
+
+// ===========================================================================
+// dx = g W^: tiles of 128 tokens by 256 inputs, one CTA each.  Warp 0 loads
+// (TMA, two stages of 64 of the N reduction: 128 + 256 rows of hi and lo),
+// warp 1 issues the MMAs, warps 2-5 write the sums out.  Every wait is bounded.
+// ===========================================================================
+constexpr int kDxTok = 128, kDxCol = 256;
+constexpr int kDxStages = 2;
+constexpr uint32_t kDxA = kDxTok * 128, kDxB = kDxCol * 128;      // one of hi, lo
+constexpr uint32_t kDxStage = 2 * (kDxA + kDxB);
+constexpr size_t kDxSmem = 1024 + (size_t)kDxStages * kDxStage + 1024;  // barriers, stages, alignment
+constexpr int kDxThreads = 6 * 32;
+
+__global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, const __grid_constant__ CUtensorMap gmap,
+                                                           const __grid_constant__ CUtensorMap wmap) {
+  extern __shared__ unsigned char dsm_raw[];
+  unsigned char *dsm = dsm_raw + (1024 - (smem_u32(dsm_raw) & 1023)) % 1024;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t *full = reinterpret_cast<uint64_t *>(dsm), *empty = full + kDxStages, *done = empty + kDxStages;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  unsigned char *buf = dsm + 1024;
+  const int k0 = blockIdx.x * kDxCol, t0 = blockIdx.y * kDxTok;
+  const int S = (a.N + 63) / 64;
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < kDxStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    mbar_init(done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, kDxCol);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int j = 0; j < S; ++j) {
+        const int s = j % kDxStages;
+        if (j >= kDxStages && !mbar_wait(empty + s, (uint32_t)(j / kDxStages - 1) & 1u, a.status, kDetLoraEmpty,
+                                         a.wait_limit)) {
+          *abort_flag = 1;
+          break;
+        }
+        unsigned char *b = buf + s * kDxStage;
+        mbar_arrive_expect_tx(full + s, kDxStage);
+        tma_load_2d(b, &gmap, j * 128, t0, full + s);
+        tma_load_2d(b + kDxA, &gmap, j * 128 + 64, t0, full + s);
+        tma_load_2d(b + 2 * kDxA, &wmap, j * 128, k0, full + s);
+        tma_load_2d(b + 2 * kDxA + kDxB, &wmap, j * 128 + 64, k0, full + s);
+        issued = j + 1;
+        if (*abort_flag) break;
+      }
+      for (int j = max(0, issued - kDxStages); j < issued; ++j)
+        mbar_drain(full + j % kDxStages, (uint32_t)(j / kDxStages) & 1u, a.status, kDetLoraDrain);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = pf_idesc(kDxCol);
+      for (int j = 0; j < S; ++j) {
+        const int s = j % kDxStages;
+        if (!mbar_wait(full + s, (uint32_t)(j / kDxStages) & 1u, a.status, kDetLoraFull, a.wait_limit) ||
+            *abort_flag) {
+          *abort_flag = 1;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t ad = umma_desc_sw128(smem_u32(buf + s * kDxStage));
+        const uint64_t bd = umma_desc_sw128(smem_u32(buf + s * kDxStage + 2 * kDxA));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t o = (uint64_t)((k * 32) >> 4);
+          umma_f16(tmem, ad + o, bd + o, idesc, (uint32_t)(j > 0 || k > 0));
+          umma_f16(tmem, ad + o, bd + o + (kDxB >> 4), idesc, 1u);
+          umma_f16(tmem, ad + o + (kDxA >> 4), bd + o, idesc, 1u);
+        }
+        umma_commit(empty + s);
+      }
+      umma_commit(done);
+      mbar_drain(done, 0, a.status, kDetLoraDrain);
+    }
+    __syncwarp();
+  } else {
+    bool ok = true;
+    if (!mbar_wait(done, 0, a.status, kDetLoraAcc, a.wait_limit)) ok = false;
+    ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+    tc_fence_after();
+    if (ok) {
+      const int q = warp & 3, t = t0 + q * 32 + lane;
+      const float f = t < a.T ? a.gexp[t] : 0.0f;
+      float *row = a.dx + (size_t)t * a.K + k0;
+#pragma unroll 4
+      for (int c = 0; c < kDxCol; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
+        tmem_ld_wait();
+        if (t < a.T && k0 + c < a.K) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float4 *>(row + c)[i] =
+                make_float4(f * __uint_as_float(v[4 * i]), f * __uint_as_float(v[4 * i + 1]),
+                            f * __uint_as_float(v[4 * i + 2]), f * __uint_as_float(v[4 * i + 3]));
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kDxCol);
+  }
+}
+
+// dx[t][l] += sum_j v[p][j] A_a[j][l]: a CTA takes up to 16 tokens of one
+// adapter by 256 inputs (32 a warp, a lane's four consecutive ones for four
+// MMA tiles).
+template <bool BF16>
+__global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs a) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int r = a.r, K = a.K;
+  if ((int)blockIdx.x >= a.tile[a.n + 1]) return;
+  const int id = adapter_at(a.tile, a.n, blockIdx.x);
+  if (id == a.n) return;
+  const int p0 = a.off[id] + ((int)blockIdx.x - a.tile[id]) * kLoraSeg;
+  const int np = min(kLoraSeg, a.off[id + 1] - p0);
+  const int lb = blockIdx.y * 256 + warp * 32;
+  if (lb >= K) return;
+  const uint16_t *A = static_cast<const uint16_t *>(a.A) + (size_t)id * r * K + lb + 4 * g;
+  const float *v0 = a.v + (size_t)(p0 + g) * r, *v1 = a.v + (size_t)(p0 + g + 8) * r;
+  const bool in0 = g < np, in1 = g + 8 < np;
+  float acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+  for (int j = 0; j < r; j += 8) {
+    const uint2 wa = __ldg(reinterpret_cast<const uint2 *>(A + (size_t)(j + q) * K));
+    const uint2 wb = __ldg(reinterpret_cast<const uint2 *>(A + (size_t)(j + q + 4) * K));
+    const float2 a0 = half2_values<BF16>(wa.x), a1 = half2_values<BF16>(wa.y);
+    const float2 b0 = half2_values<BF16>(wb.x), b1 = half2_values<BF16>(wb.y);
+    const float fa[4] = {a0.x, a0.y, a1.x, a1.y}, fb[4] = {b0.x, b0.y, b1.x, b1.y};
+    Tf32Pair e[4];
+    e[0] = split_tf32(in0 ? v0[j + q] : 0.0f);
+    e[1] = split_tf32(in1 ? v1[j + q] : 0.0f);
+    e[2] = split_tf32(in0 ? v0[j + q + 4] : 0.0f);
+    e[3] = split_tf32(in1 ? v1[j + q + 4] : 0.0f);
+    const uint32_t hi[4] = {e[0].hi, e[1].hi, e[2].hi, e[3].hi}, lo[4] = {e[0].lo, e[1].lo, e[2].lo, e[3].lo};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      mma_tf32(acc[i], hi, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
+      mma_tf32(acc[i], lo, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
+    }
+  }
+  if (lb + 8 * q >= K) return;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (!(h ? in1 : in0)) continue;
+    float4 *o = reinterpret_cast<float4 *>(a.dx + (size_t)a.perm[p0 + g + 8 * h] * K + lb + 8 * q);
+    float4 x = o[0], y = o[1];
+    x.x += acc[0][2 * h], x.y += acc[1][2 * h], x.z += acc[2][2 * h], x.w += acc[3][2 * h];
+    y.x += acc[0][2 * h + 1], y.y += acc[1][2 * h + 1], y.z += acc[2][2 * h + 1], y.w += acc[3][2 * h + 1];
+    o[0] = x;
+    o[1] = y;
+  }
+}
+
+template <int RM>
+cudaError_t outer_rows(const LoraArgs &a, const float *left, int by_token, const float *right, int L, float *out,
+                       int l_major, cudaStream_t s) {
+  const dim3 grid((unsigned)((L + kOuterL - 1) / kOuterL), (unsigned)a.n, (unsigned)((a.r + kOuterJ - 1) / kOuterJ));
+  k_lora_outer<RM><<<grid, 256, 0, s>>>(a, left, by_token, right, L, out, l_major);
+  return cudaGetLastError();
+}
+
+cudaError_t outer(const LoraArgs &a, const float *left, int by_token, const float *right, int L, float *out,
+                  int l_major, cudaStream_t s) {
+  if (a.r <= 16) return outer_rows<1>(a, left, by_token, right, L, out, l_major, s);
+  if (a.r <= 32) return outer_rows<2>(a, left, by_token, right, L, out, l_major, s);
+  return outer_rows<4>(a, left, by_token, right, L, out, l_major, s);
+}
+
+cudaError_t base_dx(const LoraArgs &a, cudaStream_t s) {
+  const int Np = (a.N + 63) / 64 * 64;
+  CUtensorMap gmap, wmap;
+  cudaError_t err = make_f16_map(&gmap, a.gs, (uint64_t)a.T, 2 * (uint64_t)Np, kDxTok);
+  if (err == cudaSuccess) err = make_f16_map(&wmap, a.wt, (uint64_t)a.K, 2 * (uint64_t)Np, kDxCol);
+  if (err != cudaSuccess) return err;
+  static int smem_set[64] = {0};
+  err = ensure_smem(k_lora_dx, kDxSmem, smem_set);
+  if (err != cudaSuccess) return err;
+  k_lora_wexp<<<(unsigned)((a.N + 7) / 8), 256, 0, s>>>(a);
+  k_lora_wt<<<dim3((unsigned)(Np / 64), (unsigned)(a.K / 64)), 256, 0, s>>>(a);
+  k_lora_gsplit<<<(unsigned)a.T, 256, 0, s>>>(a);
+  k_lora_dx<<<dim3((unsigned)((a.K + kDxCol - 1) / kDxCol), (unsigned)((a.T + kDxTok - 1) / kDxTok)), kDxThreads,
+              kDxSmem, s>>>(a, gmap, wmap);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_lora_bwd(const LoraArgs &a, cudaStream_t s) {
+  cudaError_t err = launch_lora_sort(a, s);
+  const bool any = a.T > 0 && a.n > 0;
+  if (err == cudaSuccess && any && (a.dx != nullptr || a.dA != nullptr))
+    err = launch_lora_shrink(a, a.g, a.N, a.B, true, a.v, nullptr, s);
+  if (err == cudaSuccess && any && a.dB != nullptr && a.u == nullptr)
+    err = launch_lora_shrink(a, a.x, a.K, a.A, false, a.us, nullptr, s);
+  if (err == cudaSuccess && a.n > 0 && a.dA != nullptr) err = outer(a, a.v, 0, a.x, a.K, a.dA, 0, s);
+  if (err == cudaSuccess && a.n > 0 && a.dB != nullptr)
+    err = a.u != nullptr ? outer(a, a.u, 1, a.g, a.N, a.dB, 1, s) : outer(a, a.us, 0, a.g, a.N, a.dB, 1, s);
+  if (err != cudaSuccess || a.dx == nullptr || a.T == 0) return err;
+  err = base_dx(a, s);
+  if (err != cudaSuccess || a.n == 0) return err;
+  const dim3 grid((unsigned)((a.T + kLoraSeg - 1) / kLoraSeg + a.n), (unsigned)((a.K + 255) / 256));
+  if (a.bf16) k_lora_expand<true><<<grid, 256, 0, s>>>(a);
+  else k_lora_expand<false><<<grid, 256, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace moe
