@@ -292,7 +292,10 @@ typedef struct moe_lora_dims {
 size_t moe_lora_workspace_bytes(const moe_lora_dims *dims, int32_t T_max, int32_t backward);
 
 /* out[t] = W^ x^_t + scale_a * B_a (A_a x_t), a = adapter[t]: x^ the Q8_0 codes
- * of x times their scales, as in the layer; the adapters see x itself.
+ * of x times their scales (the format of moe_quant_q8_0, the scale taken as
+ * amax times fp32's 1/127: within a unit in the last place of amax/127, so that
+ * a code may differ by one where x/d lies that close to a half-integer); the
+ * adapters see x itself.
  * x [T][K] fp32, out [T][N] fp32, u_opt [T][rank] fp32 or NULL: A_a x_t (0 for
  * tokens without an adapter), which the backward takes.  x, W, A, B and out
  * 16-byte aligned; out and u_opt overlap no input.  Block sums are exact

@@ -65,6 +65,7 @@ enum Detail : int32_t {
   kDetLoraEmpty = 51,
   kDetLoraAcc = 52,
   kDetLoraDrain = 53,
+  kDetLoraFree = 54,
 };
 
 // The wait limit kernels launched now take for their work waits (set by

@@ -46,12 +46,14 @@ __device__ __forceinline__ float *xs_at(float *xs, int64_t pos, int G, int g, in
 }
 
 // Q8_0 of four elements (8 lanes share a 32-block): the codes packed, and for
-// the block's first lane its scale and starting value.
+// the block's first lane its scale and starting value.  The scale is the
+// product with fp32's 1/127, as tensor libraries evaluate a division by a
+// constant: at most a unit in the last place from amax / 127.
 __device__ __forceinline__ uint32_t quant4(const float4 v, float &d, int &c) {
   float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
   for (int off = 4; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-  d = fdiv(m, 127.0f);
+  d = fmul(m, 1.0f / 127.0f);
   const int q0 = q8_code(v.x, d), q1 = q8_code(v.y, d), q2 = q8_code(v.z, d), q3 = q8_code(v.w, d);
   int s = q0 + q1 + q2 + q3;
 #pragma unroll
@@ -375,11 +377,12 @@ __global__ void __launch_bounds__(256) k_lora_shrink(const LoraArgs a, const flo
             b[0] = e.x, b[1] = e.y, b[2] = f.x, b[3] = f.y;
           }
         }
-#pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          mma_tf32(acc[j], hi[m], __float_as_uint(b[2 * m]), __float_as_uint(b[2 * m + 1]));
-          mma_tf32(acc[j], lo[m], __float_as_uint(b[2 * m]), __float_as_uint(b[2 * m + 1]));
-        }
+        float t[4];
+        mma_tf32_zero(t, lo[0], __float_as_uint(b[0]), __float_as_uint(b[1]));
+        mma_tf32(t, lo[1], __float_as_uint(b[2]), __float_as_uint(b[3]));
+        mma_tf32(t, hi[0], __float_as_uint(b[0]), __float_as_uint(b[1]));
+        mma_tf32(t, hi[1], __float_as_uint(b[2]), __float_as_uint(b[3]));
+        add4(acc[j], t);
       }
     }
   }
@@ -557,8 +560,10 @@ __global__ void __launch_bounds__(C::THREADS) k_lora_gemm(const LoraArgs a) {
           const Tf32Pair x = split_tf32(u.x), y = split_tf32(u.y);
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            mma_tf32(o[i][j], af[i], x.hi, y.hi);
-            mma_tf32(o[i][j], af[i], x.lo, y.lo);
+            float t[4];
+            mma_tf32_zero(t, af[i], x.lo, y.lo);
+            mma_tf32(t, af[i], x.hi, y.hi);
+            add4(o[i][j], t);
           }
         }
       }

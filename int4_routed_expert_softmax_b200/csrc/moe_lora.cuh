@@ -51,6 +51,21 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The tensor cores truncate their fp32 sums, so a long chain of MMAs into one
+// accumulator shrinks it by about 2^-24 of its size each time (measured: 1.2e-5
+// after 200).  Sums therefore start at zero for a few MMAs and are added to
+// their total by ordinary fp32 additions.
+__device__ __forceinline__ void mma_tf32_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void add4(float (&d)[4], const float (&t)[4]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) d[c] += t[c];
+}
+
 // ------------------------------------------------------------------ integer products
 // Block sums: D[16][8] = A[16][32] (unsigned bytes) B[32][8] (signed bytes) + C,
 // C the same for every row.  Lane 4 g + q holds bytes 4q .. 4q + 3 and

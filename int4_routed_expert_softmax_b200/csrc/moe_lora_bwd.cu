@@ -99,9 +99,11 @@ __global__ void __launch_bounds__(256) k_lora_outer(const LoraArgs a, const floa
       const uint32_t hi[4] = {e[0].hi, e[1].hi, e[2].hi, e[3].hi}, lw[4] = {e[0].lo, e[1].lo, e[2].lo, e[3].lo};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        mma_tf32(acc[m][i], hi, ba[i].hi, bb[i].hi);
-        mma_tf32(acc[m][i], hi, ba[i].lo, bb[i].lo);
-        mma_tf32(acc[m][i], lw, ba[i].hi, bb[i].hi);
+        float t[4];
+        mma_tf32_zero(t, hi, ba[i].lo, bb[i].lo);
+        mma_tf32(t, lw, ba[i].hi, bb[i].hi);
+        mma_tf32(t, hi, ba[i].hi, bb[i].hi);
+        add4(acc[m][i], t);
       }
     }
   }
@@ -234,37 +236,47 @@ __global__ void __launch_bounds__(256) k_lora_gsplit(const LoraArgs a) {
 // ===========================================================================
 // dx = g W^: tiles of 128 tokens by 256 inputs, one CTA each.  Warp 0 loads
 // (TMA, two stages of 64 of the N reduction: 128 + 256 rows of hi and lo),
-// warp 1 issues the MMAs, warps 2-5 write the sums out.  Every wait is bounded.
+// warp 1 issues the MMAs, warps 2-9 hold the sums in registers: a warp has one
+// quarter of the tokens (its TMEM lanes) by half of the inputs.  They add the
+// accumulator every kDxFlush stages, two accumulators taking turns, because
+// the tensor cores truncate (one accumulator over N = 6144 was off by 2.2e-5;
+// 24 MMAs lose 4e-7).  Every wait is bounded.
 // ===========================================================================
 constexpr int kDxTok = 128, kDxCol = 256;
 constexpr int kDxStages = 2;
+constexpr int kDxFlush = 2;
 constexpr uint32_t kDxA = kDxTok * 128, kDxB = kDxCol * 128;      // one of hi, lo
 constexpr uint32_t kDxStage = 2 * (kDxA + kDxB);
 constexpr size_t kDxSmem = 1024 + (size_t)kDxStages * kDxStage + 1024;  // barriers, stages, alignment
-constexpr int kDxThreads = 6 * 32;
+constexpr int kDxThreads = 10 * 32;
 
 __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, const __grid_constant__ CUtensorMap gmap,
                                                            const __grid_constant__ CUtensorMap wmap) {
   extern __shared__ unsigned char dsm_raw[];
   unsigned char *dsm = dsm_raw + (1024 - (smem_u32(dsm_raw) & 1023)) % 1024;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint64_t *full = reinterpret_cast<uint64_t *>(dsm), *empty = full + kDxStages, *done = empty + kDxStages;
+  uint64_t *full = reinterpret_cast<uint64_t *>(dsm), *empty = full + kDxStages;
+  uint64_t *accfull = empty + kDxStages, *accfree = accfull + 2, *done = accfree + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   unsigned char *buf = dsm + 1024;
   const int k0 = blockIdx.x * kDxCol, t0 = blockIdx.y * kDxTok;
-  const int S = (a.N + 63) / 64;
+  const int S = (a.N + 63) / 64, C = (S + kDxFlush - 1) / kDxFlush;
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int s = 0; s < kDxStages; ++s) {
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(accfull + s, 1);
+      mbar_init(accfree + s, 8);
+    }
     mbar_init(done, 1);
     fence_barrier_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, kDxCol);
+    tmem_alloc(tmem_slot, 2 * kDxCol);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -298,57 +310,72 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
     if (lane == 0) {
       const uint32_t idesc = pf_idesc(kDxCol);
       for (int j = 0; j < S; ++j) {
-        const int s = j % kDxStages;
+        const int s = j % kDxStages, c = j / kDxFlush;
+        const bool first = j % kDxFlush == 0;
         if (!mbar_wait(full + s, (uint32_t)(j / kDxStages) & 1u, a.status, kDetLoraFull, a.wait_limit) ||
+            (first && c >= 2 &&
+             !mbar_wait(accfree + (c & 1), (uint32_t)(c / 2 - 1) & 1u, a.status, kDetLoraFree, a.wait_limit)) ||
             *abort_flag) {
           *abort_flag = 1;
           break;
         }
         tc_fence_after();
+        const uint32_t d = tmem + (uint32_t)((c & 1) * kDxCol);
         const uint64_t ad = umma_desc_sw128(smem_u32(buf + s * kDxStage));
         const uint64_t bd = umma_desc_sw128(smem_u32(buf + s * kDxStage + 2 * kDxA));
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint64_t o = (uint64_t)((k * 32) >> 4);
-          umma_f16(tmem, ad + o, bd + o, idesc, (uint32_t)(j > 0 || k > 0));
-          umma_f16(tmem, ad + o, bd + o + (kDxB >> 4), idesc, 1u);
-          umma_f16(tmem, ad + o + (kDxA >> 4), bd + o, idesc, 1u);
+          umma_f16(d, ad + o, bd + o + (kDxB >> 4), idesc, (uint32_t)(!first || k > 0));
+          umma_f16(d, ad + o + (kDxA >> 4), bd + o, idesc, 1u);
+          umma_f16(d, ad + o, bd + o, idesc, 1u);
         }
         umma_commit(empty + s);
+        if (j % kDxFlush == kDxFlush - 1 || j == S - 1) umma_commit(accfull + (c & 1));
       }
       umma_commit(done);
       mbar_drain(done, 0, a.status, kDetLoraDrain);
     }
     __syncwarp();
   } else {
-    bool ok = true;
-    if (!mbar_wait(done, 0, a.status, kDetLoraAcc, a.wait_limit)) ok = false;
-    ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
-    tc_fence_after();
-    if (ok) {
-      const int q = warp & 3, t = t0 + q * 32 + lane;
-      const float f = t < a.T ? a.gexp[t] : 0.0f;
-      float *row = a.dx + (size_t)t * a.K + k0;
-#pragma unroll 4
-      for (int c = 0; c < kDxCol; c += 16) {
-        uint32_t v[16];
-        tmem_ld16(tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)c, v);
-        tmem_ld_wait();
-        if (t < a.T && k0 + c < a.K) {
+    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, half of the inputs
+    const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * (kDxCol / 2));
+    float acc[kDxCol / 2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<float4 *>(row + c)[i] =
-                make_float4(f * __uint_as_float(v[4 * i]), f * __uint_as_float(v[4 * i + 1]),
-                            f * __uint_as_float(v[4 * i + 2]), f * __uint_as_float(v[4 * i + 3]));
-        }
+    for (int i = 0; i < kDxCol / 2; ++i) acc[i] = 0.0f;
+    bool ok = true;
+    for (int c = 0; c < C && ok; ++c) {
+      const bool got = mbar_wait(accfull + (c & 1), (uint32_t)(c / 2) & 1u, a.status, kDetLoraAcc, a.wait_limit);
+      ok = __all_sync(0xffffffffu, got && *abort_flag == 0);
+      if (!ok) break;
+      tc_fence_after();
+#pragma unroll
+      for (int i = 0; i < kDxCol / 2; i += 16) {
+        uint32_t v[16];
+        tmem_ld16(at + (uint32_t)((c & 1) * kDxCol + i), v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) acc[i + x] += __uint_as_float(v[x]);
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(accfree + (c & 1));
     }
-    tc_fence_before();
+    if (!ok) *abort_flag = 1;
+    const int t = t0 + q * 32 + lane, kc = k0 + half * (kDxCol / 2);
+    if (ok && t < a.T) {
+      const float f = a.gexp[t];
+      float *row = a.dx + (size_t)t * a.K + kc;
+#pragma unroll
+      for (int i = 0; i < kDxCol / 2; i += 4)
+        if (kc + i < a.K)
+          *reinterpret_cast<float4 *>(row + i) = make_float4(f * acc[i], f * acc[i + 1], f * acc[i + 2], f * acc[i + 3]);
+    }
   }
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kDxCol);
+    tmem_dealloc(tmem, 2 * kDxCol);
   }
 }
 
@@ -388,8 +415,10 @@ __global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs a) {
     const uint32_t hi[4] = {e[0].hi, e[1].hi, e[2].hi, e[3].hi}, lo[4] = {e[0].lo, e[1].lo, e[2].lo, e[3].lo};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      mma_tf32(acc[i], hi, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
-      mma_tf32(acc[i], lo, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
+      float t[4];
+      mma_tf32_zero(t, lo, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
+      mma_tf32(t, hi, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
+      add4(acc[i], t);
     }
   }
   if (lb + 8 * q >= K) return;
