@@ -60,7 +60,7 @@ LoraLayout lora_layout(const moe_lora_dims &p, int T, bool backward) {
     L.wexp = seg(2 * N * 4);
   } else {
     L.xq = seg(Tp * K);
-    L.xs = seg(Tp / 2 * (K / 64) * 32);
+    L.xs = seg(Tp / 2 * (K / 64) * kXs * 4);
     L.upart = seg((K + kLoraSlice - 1) / kLoraSlice * (size_t)kLoraSmallT * r * 4);
   }
   L.total = o;
@@ -192,7 +192,9 @@ int moe_lora_backward(const moe_lora_dims *dims, int32_t T, const float *g, cons
   a.gs = at<void>(ws, L.gs);
   a.gexp = at<float>(ws, L.gexp);
   a.wexp = at<float>(ws, L.wexp);
-  return cuda_status(launch_lora_bwd(a, static_cast<cudaStream_t>(stream)));
+  const int sms = moe_device_sms();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  return cuda_status(launch_lora_bwd(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_balance_workspace_bytes(const moe_dims *dims, int32_t T_max, int32_t S_max) {

@@ -323,7 +323,8 @@ constexpr int kLoraSmallT = 32;      // the largest batch the token-order kernel
 constexpr int kLoraSlice = 512;      // inputs per CTA of their first kernel
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = 4096;
-constexpr int kLoraTile = 128;       // sorted positions are padded to this many
+constexpr int kLoraTile = 128;       // rows of the workspace are padded to this many tokens
+constexpr int kXs = 12;              // words per 64-group of two tokens: scales, starting values (moe_lora.cu)
 constexpr int kLoraSeg = 16;         // tokens of one adapter per tile of the per-adapter kernels
 
 struct LoraArgs {
@@ -335,10 +336,9 @@ struct LoraArgs {
   const float *scale;       // [n]
   const int32_t *adapter;   // [T]
   float *out, *u;           // [T][N], [T][r] or null
-  // workspace; rows by position: the token itself in token order, else its place among the
-  // tokens sorted by adapter
+  // workspace; a position is a token's place among the tokens sorted by adapter
   int8_t *xq;               // [Tp][K] Q8_0 codes
-  float *xs;                // [Tp / 2][K / 64][8] scales and code sums of two positions (moe_lora.cu)
+  float *xs;                // [Tp / 2][K / 64][kXs] scales and starting values of two tokens
   float *upart;             // [slices][T][r] partial A x (token order)
   float *us;                // [Tp][r] scale * A x by sorted position
   int32_t *perm, *off, *tile;  // sorted order: token of each position, first position and tile per adapter
@@ -354,7 +354,7 @@ struct LoraArgs {
 };
 cudaError_t launch_lora_small(const LoraArgs &a, cudaStream_t s);
 cudaError_t launch_lora_large(const LoraArgs &a, int sms, cudaStream_t s);
-cudaError_t launch_lora_bwd(const LoraArgs &a, cudaStream_t s);
+cudaError_t launch_lora_bwd(const LoraArgs &a, int sms, cudaStream_t s);
 
 // Offsets of the union mailbox (mapped pinned host memory the routing kernel
 // writes for the tiered cache): sequence number, union size, union.

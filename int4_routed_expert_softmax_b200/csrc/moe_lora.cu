@@ -26,23 +26,28 @@
 //   k_lora_proj  : 16 rows of W per CTA, its eight warps splitting the inputs;
 //                  the weights are loaded into registers before the wait for
 //                  k_lora_in, so that the two overlap.
-// Larger ones: tokens sorted by adapter.
-//   k_lora_sort  : counting sort of the tokens by adapter;
-//   k_lora_quant : Q8_0 of x by sorted position;
-//   k_lora_shrink: scale A x, 16 tokens of one adapter per CTA (tf32 hi + lo);
-//   k_lora_gemm  : tiles of W rows by sorted tokens; the adapters of the
-//                  tile's tokens are added in its epilogue by tf32 MMAs on the
-//                  same accumulators.
+// Larger ones: four launches, each started while the one before it ends.
+//   k_lora_prep  : Q8_0 of x, and a counting sort of the tokens by adapter;
+//   k_lora_shrink: scale A x, 16 tokens of one adapter per cluster (tf32 hi + lo);
+//   k_lora_gemm  : the base product, tiles of W rows by tokens;
+//   k_lora_expand: adds B (scale A x), 16 tokens of one adapter per CTA.
+#include <cooperative_groups.h>
+
 #include "moe_lora.cuh"
 
 namespace moe {
 namespace {
 
-// Scales and code sums of positions 2i and 2i + 1 for group g, at
-// xs + (i * G + g) * 8: d of block 0, d of block 1, then the MMA's starting
-// values of block 0 and block 1, each for the two positions.
-__device__ __forceinline__ float *xs_at(float *xs, int64_t pos, int G, int g, int what) {
-  return xs + ((pos >> 1) * G + g) * 8 + 2 * what + (pos & 1);
+// Scales and starting values of tokens 2i and 2i + 1 for group g, kXs words at
+// xs + (i * G + g) * kXs: d of block 0 for the two tokens, d of block 1, then
+// block 0's starting values c as the MMA's four accumulators take them
+// (c, c', c, c'), and block 1's.
+__device__ __forceinline__ void store_xs(float *xs, int t, int G, int k, float d, int c) {
+  float *p = xs + ((int64_t)(t >> 1) * G + (k >> 6)) * kXs + (t & 1);
+  const int b = (k >> 5) & 1;
+  p[2 * b] = d;
+  p[4 + 4 * b] = __int_as_float(c);
+  p[6 + 4 * b] = __int_as_float(c);
 }
 
 // Q8_0 of four elements (8 lanes share a 32-block): the codes packed, and for
@@ -81,11 +86,7 @@ __global__ void __launch_bounds__(128) k_lora_in(const LoraArgs a) {
   const uint32_t q = quant4(v, d, c);
   if (k < a.K) {
     *reinterpret_cast<uint32_t *>(a.xq + (size_t)t * a.K + k) = q;
-    if ((tid & 7) == 0) {
-      const int b = (k >> 5) & 1;
-      *xs_at(a.xs, t, G, k >> 6, b) = d;
-      *xs_at(a.xs, t, G, k >> 6, 2 + b) = __int_as_float(c);
-    }
+    if ((tid & 7) == 0) store_xs(a.xs, t, G, k, d, c);
   }
   if (id == a.n) return;
   *reinterpret_cast<float4 *>(xsm + 4 * tid) = v;
@@ -117,16 +118,23 @@ __global__ void __launch_bounds__(128) k_lora_in(const LoraArgs a) {
 
 constexpr int kProjPre = 12;  // groups a warp holds in registers (12 * 8 warps * 64 = 6144 inputs)
 
-// Accumulates one 64-group of a 16-row tile against eight columns.
-// wl, wh: 8 packed bytes of rows g and g + 8; b0, b1: the columns' codes.
-__device__ __forceinline__ void group_mma(f32x2 (&acc)[2], const uint2 wl, const uint2 wh, const uint2 b0,
-                                          const uint2 b1, const float4 d, const float4 c, f32x2 s0, f32x2 s1) {
+// The bytes of a 64-group that a lane holds of two rows, as the A operands of
+// the group's two blocks (low nibbles: block 0; high: block 1).
+struct NibblePair {
+  uint32_t lo[4], hi[4];
+};
+__device__ __forceinline__ NibblePair nibbles(const uint2 l, const uint2 h) {
   constexpr uint32_t kLow = 0x0F0F0F0Fu;
+  return NibblePair{{l.x & kLow, h.x & kLow, l.y & kLow, h.y & kLow},
+                    {(l.x >> 4) & kLow, (h.x >> 4) & kLow, (l.y >> 4) & kLow, (h.y >> 4) & kLow}};
+}
+
+// Accumulates one 64-group of a 16-row tile against eight columns.
+__device__ __forceinline__ void group_mma(f32x2 (&acc)[2], const NibblePair &w, const uint2 b0, const uint2 b1,
+                                          const float4 d, const float4 c0, const float4 c1, f32x2 s0, f32x2 s1) {
   int p[4], q[4];
-  mma_u8s8(p, wl.x & kLow, wh.x & kLow, wl.y & kLow, wh.y & kLow, b0.x, b0.y, __float_as_int(c.x),
-           __float_as_int(c.y));
-  mma_u8s8(q, (wl.x >> 4) & kLow, (wh.x >> 4) & kLow, (wl.y >> 4) & kLow, (wh.y >> 4) & kLow, b1.x, b1.y,
-           __float_as_int(c.z), __float_as_int(c.w));
+  mma_u8s8(p, w.lo, b0, c0);
+  mma_u8s8(q, w.hi, b1, c1);
   const f32x2 m = pack2(-kMagic, -kMagic);
   const f32x2 d0 = pack2(d.x, d.y), d1 = pack2(d.z, d.w);
   const f32x2 tl = fma2(add2(pack2i(q[0], q[1]), m), d1, mul2(add2(pack2i(p[0], p[1]), m), d0));
@@ -179,12 +187,13 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
       if (g < G) {
         const float s0 = __half2float(ssc[gq * Gp + g]), s1 = __half2float(ssc[(gq + 8) * Gp + g]);
         const f32x2 p0 = pack2(s0, s0), p1 = pack2(s1, s1);
+        const NibblePair w = nibbles(wl[i], wh[i]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
           const int8_t *cq = a.xq + (size_t)(j * 8 + gq) * a.K + (size_t)g * 64 + q4 * 8;
           const uint2 b0 = *reinterpret_cast<const uint2 *>(cq), b1 = *reinterpret_cast<const uint2 *>(cq + 32);
-          const float4 *x4 = reinterpret_cast<const float4 *>(a.xs + ((size_t)(j * 4 + q4) * G + g) * 8);
-          group_mma(acc[j], wl[i], wh[i], b0, b1, x4[0], x4[1], p0, p1);
+          const float4 *x4 = reinterpret_cast<const float4 *>(a.xs + ((size_t)(j * 4 + q4) * G + g) * kXs);
+          group_mma(acc[j], w, b0, b1, x4[0], x4[1], x4[2], p0, p1);
         }
       }
     }
@@ -236,25 +245,38 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
 // ===========================================================================
 // sorted batches
 // ===========================================================================
-// One CTA.  off[a]: first sorted position of adapter a (a = n: the tokens
-// without one), off[n + 1] = T; tile[a]: first kLoraSeg-token tile of adapter
-// a, tile[n + 1] the number of tiles.  The sort is stable, so that every sum
-// over an adapter's tokens has one order.  The placing pass runs in one warp,
-// 32 tokens at a time.
-__global__ void __launch_bounds__(1024) k_lora_sort(const LoraArgs a) {
-  extern __shared__ int cnt[];  // [n + 1]
+// off[a]: first sorted position of adapter a (a = n: the tokens without one),
+// off[n + 1] = T; tile[a]: first kLoraSeg-token tile of adapter a, tile[n + 1]
+// the number of tiles.  Stable, so that every sum over an adapter's tokens has
+// one order: `warps` warps of one CTA count runs of consecutive tokens in
+// tables of their own, the tables are summed up over the warps and the
+// adapters, and the warps place their runs.
+__device__ void sort_tokens(const LoraArgs &a, int *tab, int warps) {
   __shared__ int wsum[2][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int bins = a.n + 1;
-  if (tid < 4 && a.status != nullptr) a.status[tid] = 0;
-  for (int i = tid; i < bins; i += 1024) cnt[i] = 0;
+  const int bins = a.n + 1, run = ((a.T + warps - 1) / warps + 31) & ~31;
+  const int t0 = min(warp * run, a.T), t1 = warp < warps ? min(t0 + run, a.T) : t0;
+  int *mine = tab + warp * bins;
+  for (int i = tid; i < warps * bins; i += 1024) tab[i] = 0;
   __syncthreads();
-  for (int t = tid; t < a.T; t += 1024) atomicAdd(cnt + adapter_of(a, t), 1);
+  for (int t = t0 + lane; t - lane < t1; t += 32) {
+    const int id = t < t1 ? adapter_of(a, t) : -1;
+    const unsigned same = __match_any_sync(0xffffffffu, id);
+    if (id >= 0 && (same & ((1u << lane) - 1u)) == 0) mine[id] += __popc(same);
+    __syncwarp();
+  }
   __syncthreads();
   int base = 0, tbase = 0;
   for (int i0 = 0; i0 < bins; i0 += 1024) {
     const int i = i0 + tid;
-    const int c = i < bins ? cnt[i] : 0, tc = (c + kLoraSeg - 1) / kLoraSeg;
+    int c = 0;
+    if (i < bins)
+      for (int w = 0; w < warps; ++w) {
+        const int v = tab[w * bins + i];
+        tab[w * bins + i] = c;
+        c += v;
+      }
+    const int tc = (c + kLoraSeg - 1) / kLoraSeg;
     int x = c, y = tc;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -269,8 +291,9 @@ __global__ void __launch_bounds__(1024) k_lora_sort(const LoraArgs a) {
       ax += wsum[0][w], ay += wsum[1][w];
     }
     if (i < bins) {
-      cnt[i] = px + x - c;
-      a.off[i] = px + x - c;
+      const int first = px + x - c;
+      for (int w = 0; w < warps; ++w) tab[w * bins + i] += first;
+      a.off[i] = first;
       a.tile[i] = py + y - tc;
     }
     base += ax, tbase += ay;
@@ -280,156 +303,255 @@ __global__ void __launch_bounds__(1024) k_lora_sort(const LoraArgs a) {
     a.off[bins] = a.T;
     a.tile[bins] = tbase;
   }
-  if (warp != 0) return;
-  int nx = lane < a.T ? adapter_of(a, lane) : -1;
-  for (int t0 = 0; t0 < a.T; t0 += 32) {
-    const int t = t0 + lane, id = nx;
-    if (t + 32 < a.T) nx = adapter_of(a, t + 32);
-    else nx = -1;
+  for (int t = t0 + lane; t - lane < t1; t += 32) {
+    const int id = t < t1 ? adapter_of(a, t) : -1;
     const unsigned same = __match_any_sync(0xffffffffu, id);
     const int rank = __popc(same & ((1u << lane) - 1u));
-    if (t < a.T) a.perm[cnt[id] + rank] = t;
+    if (id >= 0) a.perm[mine[id] + rank] = t;
     __syncwarp();
-    if (t < a.T && rank == 0) cnt[id] += __popc(same);
+    if (id >= 0 && rank == 0) mine[id] += __popc(same);
     __syncwarp();
   }
 }
 
-// A warp takes 128 inputs of one position.
-__global__ void __launch_bounds__(256) k_lora_quant(const LoraArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int per = (a.K + 127) / 128, G = a.K / 64;
+// The first kernel of a sorted call.  CTA 0 sorts the tokens by adapter; the
+// others (where `quant`) take the Q8_0 codes of x, a warp four times 128
+// inputs of a token at once.
+__global__ void __launch_bounds__(1024) k_lora_prep(const LoraArgs a, int warps) {
+  extern __shared__ int tab[];  // [warps][n + 1]
+  pdl_launch_dependents();
+  if (blockIdx.x == 0) {
+    if (threadIdx.x < 4) a.status[threadIdx.x] = 0;
+    sort_tokens(a, tab, warps);
+    return;
+  }
+  const int lane = threadIdx.x & 31, per = (a.K + 511) / 512, G = a.K / 64;
   const int64_t n = (int64_t)a.T * per;
-  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += (int64_t)gridDim.x * 8) {
-    const int pos = (int)(i / per), k = (int)(i - (int64_t)pos * per) * 128 + lane * 4;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (k < a.K) v = *reinterpret_cast<const float4 *>(a.x + (size_t)a.perm[pos] * a.K + k);
-    float d;
-    int c;
-    const uint32_t q = quant4(v, d, c);
-    if (k < a.K) {
-      *reinterpret_cast<uint32_t *>(a.xq + (size_t)pos * a.K + k) = q;
-      if ((lane & 7) == 0) {
-        const int b = (k >> 5) & 1;
-        *xs_at(a.xs, pos, G, k >> 6, b) = d;
-        *xs_at(a.xs, pos, G, k >> 6, 2 + b) = __int_as_float(c);
+  for (int64_t i = (int64_t)(blockIdx.x - 1) * 32 + (threadIdx.x >> 5); i < n; i += (int64_t)(gridDim.x - 1) * 32) {
+    const int t = (int)(i / per), k = (int)(i - (int64_t)t * per) * 512 + lane * 4;
+    float4 v[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+      v[m] = k + 128 * m < a.K ? __ldg(reinterpret_cast<const float4 *>(a.x + (size_t)t * a.K + k + 128 * m))
+                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int km = k + 128 * m;
+      float d;
+      int c;
+      const uint32_t q = quant4(v[m], d, c);
+      if (km < a.K) {
+        *reinterpret_cast<uint32_t *>(a.xq + (size_t)t * a.K + km) = q;
+        if ((lane & 7) == 0) store_xs(a.xs, t, G, km, d, c);
       }
     }
   }
 }
 
-// dst[p][j] = scale_a sum_k src[token][k] M_a(j, k): a CTA takes one tile of
-// up to 16 tokens of one adapter, its eight warps splitting k in steps of 16;
-// a lane's four consecutive k of a step serve two MMAs (their order inside a
-// sum is free, as long as both operands agree).
+// dst[p][j] = scale_a sum_k src[token][k] M_a(j, k): a cluster takes one tile
+// of up to 16 tokens of one adapter, each of its CTAs a share of k, its eight
+// warps the share's steps of 32.  A lane's four consecutive k serve two MMAs
+// (their order inside a sum is free, as long as both operands agree).  M = A:
+// lane (g, q) reads A[8 j + g][4q ..]; M = B (TR): the RT values j = g RT .. of
+// rows 4q .., so that the columns of MMA tile jt are j = RT g + jt.  The next
+// step's loads are in flight during a step's MMAs.  The CTAs' sums are joined
+// in the first one's shared memory, always in the same order.
+template <int RT, bool TR>
+struct ShrinkStep {
+  float4 x[2][2];               // [row half][16 of k]
+  uint32_t m[2][TR ? 4 * ((RT + 1) / 2) : 2 * RT];
+};
+
 template <int RT, bool BF16, bool TR>
 __global__ void __launch_bounds__(256) k_lora_shrink(const LoraArgs a, const float *src, int L, const void *M,
                                                      float *dst, float *user) {
   extern __shared__ __align__(16) float red[];  // [8][16][RT * 8]
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
-  const int r = a.r;
-  const int id = adapter_at(a.tile, a.n, blockIdx.x);
-  if ((int)blockIdx.x >= a.tile[a.n + 1]) return;
-  const int p0 = a.off[id] + ((int)blockIdx.x - a.tile[id]) * kLoraSeg;
+  const int r = a.r, share = (int)cluster.block_rank(), shares = (int)cluster.num_blocks();
+  const int tile = (int)blockIdx.x / shares;
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tile >= a.tile[a.n + 1]) return;  // one decision for the whole cluster
+  const int id = adapter_at(a.tile, a.n, tile);
+  const int p0 = a.off[id] + (tile - a.tile[id]) * kLoraSeg;
   const int np = min(kLoraSeg, a.off[id + 1] - p0);
   if (id == a.n) {
-    if (user != nullptr)
+    if (user != nullptr && share == 0)
       for (int i = tid; i < np * r; i += 256) user[(size_t)a.perm[p0 + i / r] * r + i % r] = 0.0f;
     return;
   }
   const uint16_t *Ma = static_cast<const uint16_t *>(M) + (size_t)id * r * L;
-  const float *x0 = g < np ? src + (size_t)a.perm[p0 + g] * L : nullptr;
-  const float *x1 = g + 8 < np ? src + (size_t)a.perm[p0 + g + 8] * L : nullptr;
+  const float *x0 = src + (size_t)a.perm[p0 + min(g, np - 1)] * L;
+  const float *x1 = src + (size_t)a.perm[p0 + min(g + 8, np - 1)] * L;
+  const bool in0 = g < np, in1 = g + 8 < np;
+  constexpr int RW = (RT + 1) / 2;  // TR: words of a lane's RT values of one row
+  auto load = [&](ShrinkStep<RT, TR> &s, int k32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int k = k32 + 16 * h + 4 * q;
+      const bool in = k < L;  // L is a multiple of 8: a lane's four are all in or out
+      const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      s.x[0][h] = in && in0 ? __ldg(reinterpret_cast<const float4 *>(x0 + k)) : zero;
+      s.x[1][h] = in && in1 ? __ldg(reinterpret_cast<const float4 *>(x1 + k)) : zero;
+      if (TR) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+          const uint16_t *row = Ma + (size_t)(k + m) * r + g * RT;
+          if (RT == 1) {
+            s.m[h][m] = in ? __ldg(row) : 0u;
+          } else if (RT == 2) {
+            s.m[h][m] = in && g * RT < r ? __ldg(reinterpret_cast<const uint32_t *>(row)) : 0u;
+          } else if (RT == 4) {
+            const uint2 v = in && g * RT < r ? __ldg(reinterpret_cast<const uint2 *>(row)) : make_uint2(0u, 0u);
+            s.m[h][2 * m] = v.x, s.m[h][2 * m + 1] = v.y;
+          } else {
+#pragma unroll
+            for (int c = 0; c < RT / 8; ++c) {
+              const uint4 v = in && g * RT + 8 * c < r ? __ldg(reinterpret_cast<const uint4 *>(row) + c)
+                                                       : make_uint4(0u, 0u, 0u, 0u);
+              uint32_t *w = s.m[h] + m * RW + 4 * c;
+              w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+          const uint2 v = in && j * 8 < r ? __ldg(reinterpret_cast<const uint2 *>(Ma + (size_t)(j * 8 + g) * L + k))
+                                          : make_uint2(0u, 0u);
+          s.m[h][2 * j] = v.x, s.m[h][2 * j + 1] = v.y;
+        }
+      }
+    }
+  };
   float acc[RT][4];
 #pragma unroll
   for (int j = 0; j < RT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-  const int steps = (L + 15) / 16;
-  const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
-  for (int st = warp; st < steps; st += 8) {
-    const int k = st * 16 + 4 * q;
-    const bool in = k < L;  // L is a multiple of 8: a lane's four are all in or out
-    const float4 v0 = x0 != nullptr && in ? *reinterpret_cast<const float4 *>(x0 + k) : zero;
-    const float4 v1 = x1 != nullptr && in ? *reinterpret_cast<const float4 *>(x1 + k) : zero;
-    const float f0[4] = {v0.x, v0.y, v0.z, v0.w}, f1[4] = {v1.x, v1.y, v1.z, v1.w};
-    uint32_t hi[2][4], lo[2][4];
+  auto compute = [&](const ShrinkStep<RT, TR> &s) {
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int h = 0; h < 2; ++h) {
+      const float f0[4] = {s.x[0][h].x, s.x[0][h].y, s.x[0][h].z, s.x[0][h].w};
+      const float f1[4] = {s.x[1][h].x, s.x[1][h].y, s.x[1][h].z, s.x[1][h].w};
+      uint32_t hi[2][4], lo[2][4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const Tf32Pair s0 = split_tf32(f0[2 * m + h]), s1 = split_tf32(f1[2 * m + h]);
-        hi[m][2 * h] = s0.hi, lo[m][2 * h] = s0.lo;
-        hi[m][2 * h + 1] = s1.hi, lo[m][2 * h + 1] = s1.lo;
-      }
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
-    for (int j = 0; j < RT; ++j) {
-      if (j * 8 < r) {
-        float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (in) {
-          if (TR) {
+        for (int c = 0; c < 2; ++c) {
+          const Tf32Pair s0 = split_tf32(f0[2 * m + c]), s1 = split_tf32(f1[2 * m + c]);
+          hi[m][2 * c] = s0.hi, lo[m][2 * c] = s0.lo;
+          hi[m][2 * c + 1] = s1.hi, lo[m][2 * c + 1] = s1.lo;
+        }
 #pragma unroll
-            for (int m = 0; m < 4; ++m) b[m] = half_value<BF16>(__ldg(Ma + (size_t)(k + m) * r + j * 8 + g));
-          } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2 *>(Ma + (size_t)(j * 8 + g) * L + k));
-            const float2 e = half2_values<BF16>(w.x), f = half2_values<BF16>(w.y);
-            b[0] = e.x, b[1] = e.y, b[2] = f.x, b[3] = f.y;
+      for (int j = 0; j < RT; ++j) {
+        uint32_t b[4];
+        if (TR) {
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const uint32_t w = s.m[h][m * RW + j / 2];
+            b[m] = __float_as_uint(half_value<BF16>((uint16_t)((j & 1) ? w >> 16 : w)));
           }
+        } else {
+          const float2 e = half2_values<BF16>(s.m[h][2 * j]), f = half2_values<BF16>(s.m[h][2 * j + 1]);
+          b[0] = __float_as_uint(e.x), b[1] = __float_as_uint(e.y);
+          b[2] = __float_as_uint(f.x), b[3] = __float_as_uint(f.y);
         }
         float t[4];
-        mma_tf32_zero(t, lo[0], __float_as_uint(b[0]), __float_as_uint(b[1]));
-        mma_tf32(t, lo[1], __float_as_uint(b[2]), __float_as_uint(b[3]));
-        mma_tf32(t, hi[0], __float_as_uint(b[0]), __float_as_uint(b[1]));
-        mma_tf32(t, hi[1], __float_as_uint(b[2]), __float_as_uint(b[3]));
+        mma_tf32_zero(t, lo[0], b[0], b[1]);
+        mma_tf32(t, lo[1], b[2], b[3]);
+        mma_tf32(t, hi[0], b[0], b[1]);
+        mma_tf32(t, hi[1], b[2], b[3]);
         add4(acc[j], t);
       }
     }
+  };
+  const int steps = (L + 31) / 32, stride = 8 * shares;
+  int st = share * 8 + warp;
+  if (RT <= 8) {
+    ShrinkStep<RT, TR> s[2];
+    if (st < steps) load(s[0], st * 32);
+    while (st < steps) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        if (st + stride < steps) load(s[b ^ 1], (st + stride) * 32);
+        compute(s[b]);
+        st += stride;
+        if (st >= steps) break;
+      }
+    }
+  } else {  // two steps would not fit in the registers
+    ShrinkStep<RT, TR> s;
+    for (; st < steps; st += stride) {
+      load(s, st * 32);
+      compute(s);
+    }
   }
+  // column c of tile j: rank index 8 j + c, or RT c + j
+  auto at = [](int j, int c) { return TR ? RT * c + j : 8 * j + c; };
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
-    float *o = red + (warp * 16 + g) * (RT * 8) + j * 8 + 2 * q;
-    *reinterpret_cast<float2 *>(o) = make_float2(acc[j][0], acc[j][1]);
-    *reinterpret_cast<float2 *>(o + 8 * RT * 8) = make_float2(acc[j][2], acc[j][3]);
+    float *o = red + (warp * 16 + g) * (RT * 8);
+    o[at(j, 2 * q)] = acc[j][0];
+    o[at(j, 2 * q + 1)] = acc[j][1];
+    o += 8 * RT * 8;
+    o[at(j, 2 * q)] = acc[j][2];
+    o[at(j, 2 * q + 1)] = acc[j][3];
   }
   __syncthreads();
-  const float sc = a.scale[id];
-  for (int i = tid; i < np * r; i += 256) {
-    const int p = i / r, j = i - p * r;
+  for (int i = tid; i < 16 * RT * 8; i += 256) {
     float s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) s += red[(w * 16 + p) * (RT * 8) + j];
-    dst[(size_t)(p0 + p) * r + j] = sc * s;
-    if (user != nullptr) user[(size_t)a.perm[p0 + p] * r + j] = s;
+    for (int w = 0; w < 8; ++w) s += red[w * 16 * RT * 8 + i];
+    red[i] = s;  // row 0 of the eight: read by this thread alone
   }
+  cluster.sync();
+  if (share == 0) {
+    const float sc = a.scale[id];
+    for (int i = tid; i < np * r; i += 256) {
+      const int p = i / r, j = i - p * r;
+      float s = 0.0f;
+      for (int c = 0; c < shares; ++c) s += cluster.map_shared_rank(red, c)[p * RT * 8 + j];
+      dst[(size_t)(p0 + p) * r + j] = sc * s;
+      if (user != nullptr) user[(size_t)a.perm[p0 + p] * r + j] = s;
+    }
+  }
+  cluster.sync();  // the shares stay until they have been read
 }
 
-// Tiles of BM rows of W by BN sorted positions.  Stages of two 64-groups come
-// through shared memory by cp.async; with KW = 2 one half of the warps takes
-// the first group of a stage and the other half the second, joined at the end.
-// Row strides of 96 (weights) and 160 (codes) bytes keep the fragments' 8-byte
-// reads free of bank conflicts.
+// Tiles of BM rows of W by BN tokens, in token order.  Stages of two 64-groups
+// come through shared memory by cp.async; with KW = 2 one half of the warps
+// takes the first group of a stage and the other half the second, joined at
+// the end.  Row strides of 96 (weights) and 160 (codes) bytes keep the
+// fragments' 8-byte reads free of bank conflicts.
+//
+// The kernel reads nothing of the launch right before it (k_lora_shrink; that
+// one starts it after its own wait for k_lora_prep), so it runs beside it, and
+// waits for it only before it ends: k_lora_expand, which waits for this
+// kernel, then has both results.
 template <int WM_, int WN_, int KW_, int MT_, int NT_, int STG_>
 struct GemmCfg {
   static constexpr int WM = WM_, WN = WN_, KW = KW_, MT = MT_, NT = NT_, STG = STG_;
   static constexpr int BM = WM * MT * 16, BN = WN * NT * 8, THREADS = WM * WN * KW * 32;
-  static constexpr int WB = BM * 96, CB = BN * 160, XB = BN * 32, STAGE = WB + CB + XB;
+  static constexpr int WB = BM * 96, CB = BN * 160, XB = BN * kXs * 4, STAGE = WB + CB + XB;
   static size_t smem(int G) {
-    const size_t main = (size_t)STG * STAGE + (size_t)BM * (G + 2) * 2;
+    const size_t main = (size_t)STG * STAGE + ((size_t)BM * G * 2 + 15) / 16 * 16;
     const size_t join = KW > 1 ? (size_t)(KW - 1) * BM * BN * 4 : 0;
     return main > join ? main : join;
   }
 };
 
-template <typename C, bool BF16>
+template <typename C>
 __global__ void __launch_bounds__(C::THREADS) k_lora_gemm(const LoraArgs a) {
   extern __shared__ __align__(128) unsigned char gsm[];
   constexpr int BM = C::BM, BN = C::BN, MT = C::MT, NT = C::NT;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, q4 = lane & 3;
-  const int G = a.K / 64, N = a.N, T = a.T, r = a.r, Gp = G + 2;
+  const int G = a.K / 64, N = a.N, T = a.T;
   const int wm = warp % C::WM, wn = warp / C::WM % C::WN, kw = warp / (C::WM * C::WN);
   const int n0 = blockIdx.x * BM, p0 = blockIdx.y * BN;
-  __half *ssc = reinterpret_cast<__half *>(gsm + C::STG * C::STAGE);
+  const __half *ssc = reinterpret_cast<const __half *>(gsm + C::STG * C::STAGE);  // [BM][G]
   const int S = (G + 1) / 2;
   auto load_stage = [&](int st) {
     unsigned char *b = gsm + (st % C::STG) * C::STAGE;
@@ -444,17 +566,19 @@ __global__ void __launch_bounds__(C::THREADS) k_lora_gemm(const LoraArgs a) {
       if (c < 4 * ng)
         cp_async16(b + C::WB + row * 160 + c * 16, a.xq + (size_t)(p0 + row) * a.K + (size_t)g0 * 64 + c * 16);
     }
-    for (int i = tid; i < BN * 2; i += C::THREADS) {
-      const int pr = i >> 2, gg = (i >> 1) & 1, c = i & 1;
+    // per pair of tokens kXs / 4 pieces for each group: [group][pair][kXs]
+    for (int i = tid; i < BN * (kXs / 4); i += C::THREADS) {
+      const int pr = i / (2 * (kXs / 4)), c = i - pr * (2 * (kXs / 4)), gg = c / (kXs / 4), cc = c - gg * (kXs / 4);
       if (gg < ng)
-        cp_async16(b + C::WB + C::CB + gg * (BN * 16) + pr * 32 + c * 16,
-                   a.xs + ((size_t)(p0 / 2 + pr) * G + g0 + gg) * 8 + c * 4);
+        cp_async16(b + C::WB + C::CB + (gg * (BN / 2) + pr) * (kXs * 4) + cc * 16,
+                   a.xs + ((size_t)(p0 / 2 + pr) * G + g0 + gg) * kXs + cc * 4);
     }
   };
-  const __half *sc = reinterpret_cast<const __half *>(a.W + (size_t)N * (a.K / 2));
-  for (int i = tid; i < BM * G; i += C::THREADS) {
-    const int row = i / G, g = i - row * G;
-    ssc[row * Gp + g] = sc[(size_t)min(n0 + row, N - 1) * G + g];
+  {
+    // the scales of the tile's rows, one run of bytes (n0 G 2 is a multiple of 16)
+    const unsigned char *sc = a.W + (size_t)N * (a.K / 2) + (size_t)n0 * G * 2;
+    const int bytes = min(BM, N - n0) * G * 2;  // N % 8 == 0: a multiple of 16
+    for (int i = tid; i < bytes / 16; i += C::THREADS) cp_async16(gsm + C::STG * C::STAGE + i * 16, sc + i * 16);
   }
 #pragma unroll
   for (int st = 0; st < C::STG - 1; ++st) {
@@ -478,14 +602,14 @@ __global__ void __launch_bounds__(C::THREADS) k_lora_gemm(const LoraArgs a) {
       if (C::KW == 2 && h != kw) continue;
       const int g = 2 * st + h;
       if (g >= G) break;
-      uint2 wl[MT], wh[MT];
+      NibblePair w[MT];
       f32x2 s0[MT], s1[MT];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const int row = (wm * MT + i) * 16 + gq;
-        wl[i] = *reinterpret_cast<const uint2 *>(b + row * 96 + h * 32 + q4 * 8);
-        wh[i] = *reinterpret_cast<const uint2 *>(b + (row + 8) * 96 + h * 32 + q4 * 8);
-        const float e = __half2float(ssc[row * Gp + g]), f = __half2float(ssc[(row + 8) * Gp + g]);
+        w[i] = nibbles(*reinterpret_cast<const uint2 *>(b + row * 96 + h * 32 + q4 * 8),
+                       *reinterpret_cast<const uint2 *>(b + (row + 8) * 96 + h * 32 + q4 * 8));
+        const float e = __half2float(ssc[row * G + g]), f = __half2float(ssc[(row + 8) * G + g]);
         s0[i] = pack2(e, e);
         s1[i] = pack2(f, f);
       }
@@ -494,10 +618,10 @@ __global__ void __launch_bounds__(C::THREADS) k_lora_gemm(const LoraArgs a) {
         const int col = (wn * NT + j) * 8;
         const unsigned char *cb = b + C::WB + (col + gq) * 160 + h * 64 + q4 * 8;
         const uint2 b0 = *reinterpret_cast<const uint2 *>(cb), b1 = *reinterpret_cast<const uint2 *>(cb + 32);
-        const float4 *x4 = reinterpret_cast<const float4 *>(b + C::WB + C::CB + h * (BN * 16) + (col / 2 + q4) * 32);
-        const float4 d = x4[0], c = x4[1];
+        const float4 *x4 = reinterpret_cast<const float4 *>(b + C::WB + C::CB + (h * (BN / 2) + col / 2 + q4) * (kXs * 4));
+        const float4 d = x4[0], c0 = x4[1], c1 = x4[2];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) group_mma(acc[i][j], wl[i], wh[i], b0, b1, d, c, s0[i], s1[i]);
+        for (int i = 0; i < MT; ++i) group_mma(acc[i][j], w[i], b0, b1, d, c0, c1, s0[i], s1[i]);
       }
     }
   }
@@ -516,96 +640,197 @@ __global__ void __launch_bounds__(C::THREADS) k_lora_gemm(const LoraArgs a) {
         }
     }
     __syncthreads();
-    if (kw == 1) return;
+    if (kw == 0) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        acc[i][j][0] = add2(acc[i][j][0], join[((i * NT + j) * 2) * 32]);
-        acc[i][j][1] = add2(acc[i][j][1], join[((i * NT + j) * 2 + 1) * 32]);
-      }
-  }
-  float o[MT][NT][4];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const float2 x = unpack2(acc[i][j][0]), y = unpack2(acc[i][j][1]);
-      o[i][j][0] = x.x, o[i][j][1] = x.y, o[i][j][2] = y.x, o[i][j][3] = y.y;
-    }
-  // the adapters of this warp's positions, one after the other
-  const int pw = p0 + wn * NT * 8, pe = min(pw + NT * 8, T);
-  const int nw = n0 + wm * MT * 16;
-  if (pw < pe && pw < a.off[a.n]) {
-    for (int id = adapter_at(a.off, a.n, pw); id < a.n && a.off[id] < pe; ++id) {
-      const int b0 = max(a.off[id], pw), b1 = min(a.off[id + 1], pe);
-      if (b0 >= b1) continue;
-      const uint16_t *B = static_cast<const uint16_t *>(a.B) + (size_t)id * N * r;
-      for (int k = 0; k < r; k += 8) {
-        uint32_t af[MT][4];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const int row = nw + i * 16 + gq;
-          const uint32_t w0 = __ldg(reinterpret_cast<const uint32_t *>(B + (size_t)min(row, N - 1) * r + k) + q4);
-          const uint32_t w1 = __ldg(reinterpret_cast<const uint32_t *>(B + (size_t)min(row + 8, N - 1) * r + k) + q4);
-          const float2 v0 = half2_values<BF16>(w0), v1 = half2_values<BF16>(w1);
-          af[i][0] = __float_as_uint(v0.x), af[i][1] = __float_as_uint(v1.x);
-          af[i][2] = __float_as_uint(v0.y), af[i][3] = __float_as_uint(v1.y);
-        }
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const int p = pw + j * 8 + gq;
-          float2 u = make_float2(0.0f, 0.0f);
-          if (p >= b0 && p < b1) u = *reinterpret_cast<const float2 *>(a.us + (size_t)p * r + k + 2 * q4);
-          const Tf32Pair x = split_tf32(u.x), y = split_tf32(u.y);
+          acc[i][j][0] = add2(acc[i][j][0], join[((i * NT + j) * 2) * 32]);
+          acc[i][j][1] = add2(acc[i][j][1], join[((i * NT + j) * 2 + 1) * 32]);
+        }
+    }
+  }
+  if (kw == 0) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int t = p0 + (wn * NT + j) * 8 + 2 * q4 + c;
+        if (t < T) {
+          float *row = a.out + (size_t)t * N;
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
-            float t[4];
-            mma_tf32_zero(t, af[i], x.lo, y.lo);
-            mma_tf32(t, af[i], x.hi, y.hi);
-            add4(o[i][j], t);
+            const int n = n0 + (wm * MT + i) * 16 + gq;
+            const float2 x = unpack2(acc[i][j][0]), y = unpack2(acc[i][j][1]);
+            if (n < N) row[n] = c ? x.y : x.x;
+            if (n + 8 < N) row[n + 8] = c ? y.y : y.x;
           }
         }
       }
     }
   }
+  pdl_launch_dependents();
+  pdl_wait();
+}
+
+// dst[t][l] += sum_j s[p][j] M_a(j, l): M_a(j, l) = A_a[j][l], or B_a[l][j] if
+// LM.  A CTA takes up to 16 tokens of one adapter (the MMA's rows) by 256
+// columns, a warp 32: four MMA tiles.  With M = A a lane's column of the four
+// tiles are four consecutive l (one 8-byte load per row j), with M = B a lane
+// reads two consecutive j of each column.  The loads of 32 of the rank are
+// issued together.
+template <bool BF16, bool LM>
+__global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs a, const float *s, const void *M, int L,
+                                                     float *dst) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int r = a.r, lb = blockIdx.y * 256 + warp * 32;
+  pdl_wait();
+  if ((int)blockIdx.x >= a.tile[a.n + 1] || lb >= L) return;
+  const int id = adapter_at(a.tile, a.n, blockIdx.x);
+  if (id == a.n) return;
+  const int p0 = a.off[id] + ((int)blockIdx.x - a.tile[id]) * kLoraSeg;
+  const int np = min(kLoraSeg, a.off[id + 1] - p0);
+  const uint16_t *Ma = static_cast<const uint16_t *>(M) + (size_t)id * r * L;
+  const bool in0 = g < np, in1 = g + 8 < np;
+  const float *v0 = s + (size_t)(p0 + g) * r, *v1 = s + (size_t)(p0 + g + 8) * r;
+  // this lane's outputs: LM: columns lb + 8 i + 2q, + 1 of tile i; else lb + 8q .. + 7
+  const int lo = LM ? lb + 2 * q : lb + 8 * q;
+  float *o0 = dst + (in0 ? (size_t)a.perm[p0 + g] * L : 0) + lo, *o1 = dst + (in1 ? (size_t)a.perm[p0 + g + 8] * L : 0) + lo;
+  float old[2][8];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) {
+  for (int h = 0; h < 2; ++h) {
+    const bool in = h ? in1 : in0;
+    const float *o = h ? o1 : o0;
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int p = pw + j * 8 + 2 * q4 + c;
-      if (p < T) {
-        float *row = a.out + (size_t)a.perm[p] * N;
+    for (int i = 0; i < 4; ++i) {
+      float2 v = make_float2(0.0f, 0.0f);
+      if (in && (LM ? lo + 8 * i < L : lo < L)) v = *reinterpret_cast<const float2 *>(o + (LM ? 8 * i : 2 * i));
+      old[h][2 * i] = v.x;
+      old[h][2 * i + 1] = v.y;
+    }
+  }
+  float acc[4][4];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const int n = nw + i * 16 + gq;
-          if (n < N) row[n] = o[i][j][c];
-          if (n + 8 < N) row[n + 8] = o[i][j][2 + c];
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+  for (int j0 = 0; j0 < r; j0 += 32) {
+    // LM: per 8 of j and tile one word (j = 2q, 2q + 1 of column 8 i + g); else per 8 of j two rows (q, q + 4) of 4 columns
+    uint32_t w[4][4];
+    float2 e0[4], e1[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int j = j0 + 8 * m;
+      e0[m] = e1[m] = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[m][i] = 0u;
+      if (j < r) {
+        if (LM) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (lb + 8 * i < L)
+              w[m][i] = __ldg(reinterpret_cast<const uint32_t *>(Ma + (size_t)(lb + 8 * i + g) * r + j + 2 * q));
+          if (in0) e0[m] = *reinterpret_cast<const float2 *>(v0 + j + 2 * q);
+          if (in1) e1[m] = *reinterpret_cast<const float2 *>(v1 + j + 2 * q);
+        } else {
+          if (lb + 4 * g < L) {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(Ma + (size_t)(j + q) * L + lb + 4 * g));
+            const uint2 y = __ldg(reinterpret_cast<const uint2 *>(Ma + (size_t)(j + q + 4) * L + lb + 4 * g));
+            w[m][0] = x.x, w[m][1] = x.y, w[m][2] = y.x, w[m][3] = y.y;
+          }
+          if (in0) e0[m] = make_float2(v0[j + q], v0[j + q + 4]);
+          if (in1) e1[m] = make_float2(v1[j + q], v1[j + q + 4]);
         }
       }
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      if (j0 + 8 * m >= r) break;
+      const Tf32Pair x0 = split_tf32(e0[m].x), x1 = split_tf32(e1[m].x), y0 = split_tf32(e0[m].y), y1 = split_tf32(e1[m].y);
+      const uint32_t hi[4] = {x0.hi, x1.hi, y0.hi, y1.hi}, lw[4] = {x0.lo, x1.lo, y0.lo, y1.lo};
+      float fa[4], fb[4];
+      if (LM) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = half2_values<BF16>(w[m][i]);
+          fa[i] = f.x, fb[i] = f.y;
+        }
+      } else {
+        const float2 a0 = half2_values<BF16>(w[m][0]), a1 = half2_values<BF16>(w[m][1]);
+        const float2 b0 = half2_values<BF16>(w[m][2]), b1 = half2_values<BF16>(w[m][3]);
+        fa[0] = a0.x, fa[1] = a0.y, fa[2] = a1.x, fa[3] = a1.y;
+        fb[0] = b0.x, fb[1] = b0.y, fb[2] = b1.x, fb[3] = b1.y;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float t[4];
+        mma_tf32_zero(t, lw, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
+        mma_tf32(t, hi, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
+        add4(acc[i], t);
+      }
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (!(h ? in1 : in0)) continue;
+    float *o = h ? o1 : o0;
+    if (LM) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (lo + 8 * i < L)
+          *reinterpret_cast<float2 *>(o + 8 * i) =
+              make_float2(old[h][2 * i] + acc[i][2 * h], old[h][2 * i + 1] + acc[i][2 * h + 1]);
+    } else if (lo < L) {
+      // columns lo + 0 .. 3 are this lane's first column of tiles 0 .. 3, lo + 4 .. 7 its second
+      float4 *f = reinterpret_cast<float4 *>(o);
+      f[0] = make_float4(old[h][0] + acc[0][2 * h], old[h][1] + acc[1][2 * h], old[h][2] + acc[2][2 * h],
+                         old[h][3] + acc[3][2 * h]);
+      f[1] = make_float4(old[h][4] + acc[0][2 * h + 1], old[h][5] + acc[1][2 * h + 1], old[h][6] + acc[2][2 * h + 1],
+                         old[h][7] + acc[3][2 * h + 1]);
     }
   }
 }
 
+// CTAs per tile (a power of two, at most a cluster's portable eight): enough
+// for two CTAs per SM, as long as each keeps 256 of the sum.
+int shrink_shares(int tiles, int L, int sms) {
+  int c = 1;
+  while (c < 8 && tiles * c < 2 * sms && L / (2 * c) >= 256) c *= 2;
+  return c;
+}
+
 template <int RT, bool BF16, bool TR>
-cudaError_t shrink(const LoraArgs &a, const float *src, int L, const void *M, float *dst, float *user,
+cudaError_t shrink(const LoraArgs &a, const float *src, int L, const void *M, float *dst, float *user, int sms,
                    cudaStream_t s) {
   const size_t smem = (size_t)8 * 16 * RT * 8 * 4;
   static int smem_set[64] = {0};
   cudaError_t err = ensure_smem(k_lora_shrink<RT, BF16, TR>, smem, smem_set);
   if (err != cudaSuccess) return err;
-  const int tiles = (a.T + kLoraSeg - 1) / kLoraSeg + a.n;  // at most: each adapter's last tile may be short
-  k_lora_shrink<RT, BF16, TR><<<tiles, 256, smem, s>>>(a, src, L, M, dst, user);
-  return cudaGetLastError();
+  const int tiles = lora_tiles(a);
+  const int shares = shrink_shares(tiles, L, sms);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tiles * shares));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)shares;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_lora_shrink<RT, BF16, TR>, a, src, L, M, dst, user);
 }
 
 template <bool BF16, bool TR>
-cudaError_t shrink_rank(const LoraArgs &a, const float *src, int L, const void *M, float *dst, float *user,
+cudaError_t shrink_rank(const LoraArgs &a, const float *src, int L, const void *M, float *dst, float *user, int sms,
                         cudaStream_t s) {
-  if (a.r <= 16) return shrink<2, BF16, TR>(a, src, L, M, dst, user, s);
-  if (a.r <= 32) return shrink<4, BF16, TR>(a, src, L, M, dst, user, s);
-  if (a.r <= 64) return shrink<8, BF16, TR>(a, src, L, M, dst, user, s);
-  return shrink<16, BF16, TR>(a, src, L, M, dst, user, s);
+  if (a.r <= 16) return shrink<2, BF16, TR>(a, src, L, M, dst, user, sms, s);
+  if (a.r <= 32) return shrink<4, BF16, TR>(a, src, L, M, dst, user, sms, s);
+  if (a.r <= 64) return shrink<8, BF16, TR>(a, src, L, M, dst, user, sms, s);
+  return shrink<16, BF16, TR>(a, src, L, M, dst, user, sms, s);
 }
 
 template <int NT, bool BF16>
@@ -627,39 +852,50 @@ cudaError_t small(const LoraArgs &a, cudaStream_t s) {
   return proj<4, BF16>(a, s);
 }
 
-template <typename C, bool BF16>
-cudaError_t gemm(const LoraArgs &a, cudaStream_t s) {
+template <typename C>
+cudaError_t gemm(const LoraArgs &a, bool pdl, cudaStream_t s) {
   const size_t smem = C::smem(a.K / 64);
   static int smem_set[64] = {0};
-  cudaError_t err = ensure_smem(k_lora_gemm<C, BF16>, smem, smem_set);
+  cudaError_t err = ensure_smem(k_lora_gemm<C>, smem, smem_set);
   if (err != cudaSuccess) return err;
   const dim3 grid((unsigned)((a.N + C::BM - 1) / C::BM), (unsigned)((a.T + C::BN - 1) / C::BN));
-  k_lora_gemm<C, BF16><<<grid, C::THREADS, smem, s>>>(a);
+  if (pdl) return launch_pdl(k_lora_gemm<C>, grid, dim3(C::THREADS), smem, s, a);
+  k_lora_gemm<C><<<grid, C::THREADS, smem, s>>>(a);
   return cudaGetLastError();
-}
-
-template <bool BF16>
-cudaError_t large(const LoraArgs &a, int sms, cudaStream_t s) {
-  using Big = GemmCfg<2, 4, 1, 4, 4, 3>;    // 128 x 128
-  using Small = GemmCfg<2, 2, 2, 2, 4, 3>;  // 64 x 64, two halves of K
-  const int64_t tiles = (int64_t)((a.N + 127) / 128) * ((a.T + 127) / 128);
-  return tiles >= sms ? gemm<Big, BF16>(a, s) : gemm<Small, BF16>(a, s);
 }
 
 }  // namespace
 
-cudaError_t launch_lora_sort(const LoraArgs &a, cudaStream_t s) {
-  k_lora_sort<<<1, 1024, (size_t)(a.n + 1) * 4, s>>>(a);
+cudaError_t launch_lora_prep(const LoraArgs &a, bool quant, int sms, cudaStream_t s) {
+  // tables of 32 warps where they fit, of 8 for thousands of adapters
+  const int warps = a.n < 1024 ? 32 : 8;
+  const size_t smem = (size_t)warps * (a.n + 1) * 4;
+  static int smem_set[64] = {0};
+  cudaError_t err = ensure_smem(k_lora_prep, smem, smem_set);
+  if (err != cudaSuccess) return err;
+  int64_t ctas = quant ? ((int64_t)a.T * ((a.K + 511) / 512) + 31) / 32 : 0;
+  if (ctas > 2 * sms) ctas = 2 * sms;
+  k_lora_prep<<<(unsigned)(1 + ctas), 1024, smem, s>>>(a, warps);
   return cudaGetLastError();
 }
 
 cudaError_t launch_lora_shrink(const LoraArgs &a, const float *src, int L, const void *M, bool transposed, float *dst,
-                               float *user, cudaStream_t s) {
+                               float *user, int sms, cudaStream_t s) {
   if (transposed)
-    return a.bf16 ? shrink_rank<true, true>(a, src, L, M, dst, user, s)
-                  : shrink_rank<false, true>(a, src, L, M, dst, user, s);
-  return a.bf16 ? shrink_rank<true, false>(a, src, L, M, dst, user, s)
-                : shrink_rank<false, false>(a, src, L, M, dst, user, s);
+    return a.bf16 ? shrink_rank<true, true>(a, src, L, M, dst, user, sms, s)
+                  : shrink_rank<false, true>(a, src, L, M, dst, user, sms, s);
+  return a.bf16 ? shrink_rank<true, false>(a, src, L, M, dst, user, sms, s)
+                : shrink_rank<false, false>(a, src, L, M, dst, user, sms, s);
+}
+
+cudaError_t launch_lora_expand(const LoraArgs &a, const float *v, const void *M, bool l_major, int L, float *dst,
+                               cudaStream_t s) {
+  const dim3 grid((unsigned)lora_tiles(a), (unsigned)((L + 255) / 256));
+  if (l_major)
+    return a.bf16 ? launch_pdl(k_lora_expand<true, true>, grid, dim3(256), 0, s, a, v, M, L, dst)
+                  : launch_pdl(k_lora_expand<false, true>, grid, dim3(256), 0, s, a, v, M, L, dst);
+  return a.bf16 ? launch_pdl(k_lora_expand<true, false>, grid, dim3(256), 0, s, a, v, M, L, dst)
+                : launch_pdl(k_lora_expand<false, false>, grid, dim3(256), 0, s, a, v, M, L, dst);
 }
 
 cudaError_t launch_lora_small(const LoraArgs &a, cudaStream_t s) {
@@ -667,17 +903,17 @@ cudaError_t launch_lora_small(const LoraArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_lora_large(const LoraArgs &a, int sms, cudaStream_t s) {
-  cudaError_t err = launch_lora_sort(a, s);
+  cudaError_t err = launch_lora_prep(a, true, sms, s);
+  const bool adapters = a.n > 0 || a.u != nullptr;  // without an adapter u is still written (zeros)
+  if (err == cudaSuccess && adapters) err = launch_lora_shrink(a, a.x, a.K, a.A, false, a.us, a.u, sms, s);
   if (err != cudaSuccess) return err;
-  const int64_t warps = (int64_t)a.T * ((a.K + 127) / 128);
-  const int64_t most = (int64_t)sms * 8;
-  const int64_t ctas = (warps + 7) / 8;
-  k_lora_quant<<<(unsigned)(ctas < most ? ctas : most), 256, 0, s>>>(a);
-  err = cudaGetLastError();
-  if (err != cudaSuccess) return err;
-  err = launch_lora_shrink(a, a.x, a.K, a.A, false, a.us, a.u, s);
-  if (err != cudaSuccess) return err;
-  return a.bf16 ? large<true>(a, sms, s) : large<false>(a, sms, s);
+  using Big = GemmCfg<2, 4, 1, 4, 4, 3>;    // 128 x 128
+  using Small = GemmCfg<2, 2, 2, 2, 4, 3>;  // 64 x 64, two halves of K
+  const int64_t tiles = (int64_t)((a.N + 127) / 128) * ((a.T + 127) / 128);
+  // without the shrink between them the GEMM follows the quantisation directly, and waits for it
+  err = tiles >= sms ? gemm<Big>(a, adapters, s) : gemm<Small>(a, adapters, s);
+  if (err != cudaSuccess || a.n == 0) return err;
+  return launch_lora_expand(a, a.us, a.B, true, a.N, a.out, s);
 }
 
 }  // namespace moe

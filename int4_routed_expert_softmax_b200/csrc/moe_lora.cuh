@@ -45,7 +45,7 @@ __device__ __forceinline__ Tf32Pair split_tf32(float v) {
 // A(g, q + 4), A(g + 8, q + 4); b = B(q, g), B(q + 4, g); d = D(g, 2q),
 // D(g, 2q + 1), D(g + 8, 2q), D(g + 8, 2q + 1).
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -56,7 +56,7 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 // after 200).  Sums therefore start at zero for a few MMAs and are added to
 // their total by ordinary fp32 additions.
 __device__ __forceinline__ void mma_tf32_zero(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
@@ -67,15 +67,14 @@ __device__ __forceinline__ void add4(float (&d)[4], const float (&t)[4]) {
 }
 
 // ------------------------------------------------------------------ integer products
-// Block sums: D[16][8] = A[16][32] (unsigned bytes) B[32][8] (signed bytes) + C,
-// C the same for every row.  Lane 4 g + q holds bytes 4q .. 4q + 3 and
-// 16 + 4q .. of rows g (a0, a2) and g + 8 (a1, a3) and of column g (b0, b1).
-__device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1, int c0, int c1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
+// Block sums: D[16][8] = A[16][32] (unsigned bytes) B[32][8] (signed bytes) + C.
+// Lane 4 g + q holds bytes 4q .. 4q + 3 and 16 + 4q .. of rows g (a[0], a[2])
+// and g + 8 (a[1], a[3]) and of column g (b.x, b.y); C and D like a tf32 D.
+__device__ __forceinline__ void mma_u8s8(int (&d)[4], const uint32_t (&a)[4], const uint2 b, const float4 c) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
       : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0), "r"(c1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "r"(__float_as_int(c.x)),
+        "r"(__float_as_int(c.y)), "r"(__float_as_int(c.z)), "r"(__float_as_int(c.w)));
 }
 // The sums leave the MMA as floats: started from the bit pattern of
 // 1.5 * 2^23, an integer of magnitude below 2^22 added to it is the float
@@ -160,12 +159,20 @@ inline cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// moe_lora.cu, used by the backward too
-cudaError_t launch_lora_sort(const LoraArgs &a, cudaStream_t s);
+// At most this many tiles of kLoraSeg tokens of one adapter (each adapter's
+// last tile, and that of the tokens without one, may be short).
+inline int lora_tiles(const LoraArgs &a) { return (a.T + kLoraSeg - 1) / kLoraSeg + a.n; }
+
+// moe_lora.cu, used by the backward too.  prep: the sort (and Q8_0 of x if
+// `quant`), also zeroes the status word.
+cudaError_t launch_lora_prep(const LoraArgs &a, bool quant, int sms, cudaStream_t s);
 // dst[p][j] = scale_a sum_k src[token][k] M_a(j, k) by sorted position; M_a(j, k) =
 // A_a[j][k], or B_a[k][j] if `transposed`.  user (or null): the unscaled sums
 // by token, 0 for tokens without an adapter.
 cudaError_t launch_lora_shrink(const LoraArgs &a, const float *src, int L, const void *M, bool transposed, float *dst,
-                               float *user, cudaStream_t s);
+                               float *user, int sms, cudaStream_t s);
+// dst[t][l] += sum_j v[p][j] M_a(j, l); M_a(j, l) = A_a[j][l], or B_a[l][j] if `l_major`.
+cudaError_t launch_lora_expand(const LoraArgs &a, const float *v, const void *M, bool l_major, int L, float *dst,
+                               cudaStream_t s);
 
 }  // namespace moe

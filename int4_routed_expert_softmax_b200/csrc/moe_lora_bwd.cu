@@ -7,7 +7,7 @@
 //
 // (W^ is frozen; the Q8_0 rounding of x passes gradients unchanged).
 //
-//   k_lora_sort    : tokens by adapter (moe_lora.cu);
+//   k_lora_prep    : tokens by adapter (moe_lora.cu);
 //   k_lora_shrink  : v, and u where the caller kept none (moe_lora.cu);
 //   k_lora_outer   : dA and dB, a tile of the matrix per CTA, its warps
 //                    splitting the adapter's tokens (tf32 hi + lo, three MMAs);
@@ -379,61 +379,6 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
   }
 }
 
-// dx[t][l] += sum_j v[p][j] A_a[j][l]: a CTA takes up to 16 tokens of one
-// adapter by 256 inputs (32 a warp, a lane's four consecutive ones for four
-// MMA tiles).
-template <bool BF16>
-__global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs a) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int r = a.r, K = a.K;
-  if ((int)blockIdx.x >= a.tile[a.n + 1]) return;
-  const int id = adapter_at(a.tile, a.n, blockIdx.x);
-  if (id == a.n) return;
-  const int p0 = a.off[id] + ((int)blockIdx.x - a.tile[id]) * kLoraSeg;
-  const int np = min(kLoraSeg, a.off[id + 1] - p0);
-  const int lb = blockIdx.y * 256 + warp * 32;
-  if (lb >= K) return;
-  const uint16_t *A = static_cast<const uint16_t *>(a.A) + (size_t)id * r * K + lb + 4 * g;
-  const float *v0 = a.v + (size_t)(p0 + g) * r, *v1 = a.v + (size_t)(p0 + g + 8) * r;
-  const bool in0 = g < np, in1 = g + 8 < np;
-  float acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
-  for (int j = 0; j < r; j += 8) {
-    const uint2 wa = __ldg(reinterpret_cast<const uint2 *>(A + (size_t)(j + q) * K));
-    const uint2 wb = __ldg(reinterpret_cast<const uint2 *>(A + (size_t)(j + q + 4) * K));
-    const float2 a0 = half2_values<BF16>(wa.x), a1 = half2_values<BF16>(wa.y);
-    const float2 b0 = half2_values<BF16>(wb.x), b1 = half2_values<BF16>(wb.y);
-    const float fa[4] = {a0.x, a0.y, a1.x, a1.y}, fb[4] = {b0.x, b0.y, b1.x, b1.y};
-    Tf32Pair e[4];
-    e[0] = split_tf32(in0 ? v0[j + q] : 0.0f);
-    e[1] = split_tf32(in1 ? v1[j + q] : 0.0f);
-    e[2] = split_tf32(in0 ? v0[j + q + 4] : 0.0f);
-    e[3] = split_tf32(in1 ? v1[j + q + 4] : 0.0f);
-    const uint32_t hi[4] = {e[0].hi, e[1].hi, e[2].hi, e[3].hi}, lo[4] = {e[0].lo, e[1].lo, e[2].lo, e[3].lo};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float t[4];
-      mma_tf32_zero(t, lo, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
-      mma_tf32(t, hi, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
-      add4(acc[i], t);
-    }
-  }
-  if (lb + 8 * q >= K) return;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (!(h ? in1 : in0)) continue;
-    float4 *o = reinterpret_cast<float4 *>(a.dx + (size_t)a.perm[p0 + g + 8 * h] * K + lb + 8 * q);
-    float4 x = o[0], y = o[1];
-    x.x += acc[0][2 * h], x.y += acc[1][2 * h], x.z += acc[2][2 * h], x.w += acc[3][2 * h];
-    y.x += acc[0][2 * h + 1], y.y += acc[1][2 * h + 1], y.z += acc[2][2 * h + 1], y.w += acc[3][2 * h + 1];
-    o[0] = x;
-    o[1] = y;
-  }
-}
-
 template <int RM>
 cudaError_t outer_rows(const LoraArgs &a, const float *left, int by_token, const float *right, int L, float *out,
                        int l_major, cudaStream_t s) {
@@ -468,23 +413,20 @@ cudaError_t base_dx(const LoraArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_lora_bwd(const LoraArgs &a, cudaStream_t s) {
-  cudaError_t err = launch_lora_sort(a, s);
+cudaError_t launch_lora_bwd(const LoraArgs &a, int sms, cudaStream_t s) {
+  cudaError_t err = launch_lora_prep(a, false, sms, s);
   const bool any = a.T > 0 && a.n > 0;
   if (err == cudaSuccess && any && (a.dx != nullptr || a.dA != nullptr))
-    err = launch_lora_shrink(a, a.g, a.N, a.B, true, a.v, nullptr, s);
+    err = launch_lora_shrink(a, a.g, a.N, a.B, true, a.v, nullptr, sms, s);
   if (err == cudaSuccess && any && a.dB != nullptr && a.u == nullptr)
-    err = launch_lora_shrink(a, a.x, a.K, a.A, false, a.us, nullptr, s);
+    err = launch_lora_shrink(a, a.x, a.K, a.A, false, a.us, nullptr, sms, s);
   if (err == cudaSuccess && a.n > 0 && a.dA != nullptr) err = outer(a, a.v, 0, a.x, a.K, a.dA, 0, s);
   if (err == cudaSuccess && a.n > 0 && a.dB != nullptr)
     err = a.u != nullptr ? outer(a, a.u, 1, a.g, a.N, a.dB, 1, s) : outer(a, a.us, 0, a.g, a.N, a.dB, 1, s);
   if (err != cudaSuccess || a.dx == nullptr || a.T == 0) return err;
   err = base_dx(a, s);
   if (err != cudaSuccess || a.n == 0) return err;
-  const dim3 grid((unsigned)((a.T + kLoraSeg - 1) / kLoraSeg + a.n), (unsigned)((a.K + 255) / 256));
-  if (a.bf16) k_lora_expand<true><<<grid, 256, 0, s>>>(a);
-  else k_lora_expand<false><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_lora_expand(a, a.v, a.A, false, a.K, a.dx, s);
 }
 
 }  // namespace moe
