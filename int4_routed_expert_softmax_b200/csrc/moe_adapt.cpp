@@ -32,7 +32,8 @@ int check_lora(const moe_lora_dims *p, int32_t T) {
 
 struct LoraLayout {
   size_t status, perm, off, tile, us;     // both calls
-  size_t xq, xs, upart;                   // forward
+  size_t xq, xs, upart;                   // forward, small batches
+  size_t xh, wh, xd, ws;                  // forward, larger ones
   size_t v, wt, gs, gexp, wexp;           // backward
   size_t total;
 };
@@ -59,9 +60,15 @@ LoraLayout lora_layout(const moe_lora_dims &p, int T, bool backward) {
     L.gexp = seg(Tp * 4);
     L.wexp = seg(2 * N * 4);
   } else {
-    L.xq = seg(Tp * K);
-    L.xs = seg(Tp / 2 * (K / 64) * kXs * 4);
+    L.xq = seg(kLoraSmallT * K);
+    L.xs = seg((size_t)kLoraSmallT / 2 * (K / 64) * kXs * 4);
     L.upart = seg((K + kLoraSlice - 1) / kLoraSlice * (size_t)kLoraSmallT * r * 4);
+    if (T > kLoraSmallT) {
+      L.xh = seg(Tp * K * 2);
+      L.wh = seg(N * K * 2);
+      L.xd = seg(K / 64 * Tp * 8);
+      L.ws = seg(K / 64 * align_up(N, kLoraColTile) * 4);
+    }
   }
   L.total = o;
   return L;
@@ -161,6 +168,11 @@ int moe_lora_forward(const moe_lora_dims *dims, int32_t T, const float *x, const
   a.xq = at<int8_t>(ws, L.xq);
   a.xs = at<float>(ws, L.xs);
   a.upart = at<float>(ws, L.upart);
+  a.xh = at<__half>(ws, L.xh);
+  a.wh = at<__half>(ws, L.wh);
+  a.xd = at<float>(ws, L.xd);
+  a.ws = at<float>(ws, L.ws);
+  a.Nt = (int)align_up((size_t)dims->N, kLoraColTile);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T <= kLoraSmallT) return cuda_status(launch_lora_small(a, s));
   const int sms = moe_device_sms();

@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/moe.h"
@@ -66,6 +67,9 @@ enum Detail : int32_t {
   kDetLoraAcc = 52,
   kDetLoraDrain = 53,
   kDetLoraFree = 54,
+  kDetLoraGemmFull = 55,
+  kDetLoraGemmEmpty = 56,
+  kDetLoraGemmDrain = 57,
 };
 
 // The wait limit kernels launched now take for their work waits (set by
@@ -324,7 +328,8 @@ constexpr int kLoraSlice = 512;      // inputs per CTA of their first kernel
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = 4096;
 constexpr int kLoraTile = 128;       // rows of the workspace are padded to this many tokens
-constexpr int kXs = 12;              // words per 64-group of two tokens: scales, starting values (moe_lora.cu)
+constexpr int kLoraColTile = 256;    // and the rows of W's scales to this many columns
+constexpr int kXs = 8;               // words per 64-group of two tokens: scales, starting values (moe_lora.cu)
 constexpr int kLoraSeg = 16;         // tokens of one adapter per tile of the per-adapter kernels
 
 struct LoraArgs {
@@ -337,8 +342,11 @@ struct LoraArgs {
   const int32_t *adapter;   // [T]
   float *out, *u;           // [T][N], [T][r] or null
   // workspace; a position is a token's place among the tokens sorted by adapter
-  int8_t *xq;               // [Tp][K] Q8_0 codes
-  float *xs;                // [Tp / 2][K / 64][kXs] scales and starting values of two tokens
+  int8_t *xq;               // small batches: [T][K] Q8_0 codes
+  float *xs;                // and per two tokens and group [T / 2][K / 64][kXs] scales and starting values
+  __half *xh, *wh;          // larger ones: [T][K] codes and [N][K] weights, integers in fp16
+  float *xd, *ws;           // [K / 64][Tp][2] scales of the codes, [K / 64][Nt] of the weights
+  int Nt;                   // row length of ws: N in whole tiles
   float *upart;             // [slices][T][r] partial A x (token order)
   float *us;                // [Tp][r] scale * A x by sorted position
   int32_t *perm, *off, *tile;  // sorted order: token of each position, first position and tile per adapter

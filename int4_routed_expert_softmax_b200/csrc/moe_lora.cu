@@ -6,20 +6,13 @@
 // The base product is the layer's own definition: with exact integer block
 // sums S_b(n, t) over 32 elements,
 //   out(n, t) = sum over groups g of s(n, g) (S_2g d(t, 2g) + S_2g+1 d(t, 2g+1)).
-// One mma.sync m16n8k32 with unsigned weight nibbles and signed codes gives
-// sixteen by eight block sums at once, already in the registers that scale
-// them.  The fifth-generation tensor cores would leave them in tensor memory:
-// a block sum ends every 32 elements, so each would be read back through
-// tcgen05.ld before its scaling, and the scaling sets the pace on either
-// route.  The alternative without block sums, tcgen05 on fp16 hi / lo
-// operands, costs three MMAs per product for the same 22 bits.  Rate of the
-// integer mma.sync on this part: 1.12 POP/s (two per product).
-//
-// A nibble u is w + 8; the accumulator therefore starts at -8 times the sum
-// of the block's codes (kept beside the block's scale), and at the bits of
-// 1.5 * 2^23, which makes the sum a float for one subtraction.  The scaling
-// runs in packed pairs of columns: per 64-group and pair two subtractions, a
-// product and two fused multiply-adds.
+// Small batches take the sums from mma.sync m16n8k32 on unsigned weight nibbles
+// and signed codes: a nibble u is w + 8, so an accumulator starts at -8 times
+// the sum of the block's codes (kept beside the block's scale), and at the bits
+// of 1.5 * 2^23, which makes the sum a float for one subtraction.  Larger ones
+// take them from tcgen05 on fp16 integers (k_lora_base): there mma.sync was
+// held up by the registers its accumulators start from (seven moves per MMA,
+// 207 us for 2048 tokens by 2048 x 6144).
 //
 // Small batches (at most kLoraSmallT tokens): two launches in token order.
 //   k_lora_in    : Q8_0 of x, and partial sums of A x per slice of the inputs;
@@ -27,44 +20,38 @@
 //                  the weights are loaded into registers before the wait for
 //                  k_lora_in, so that the two overlap.
 // Larger ones: four launches, each started while the one before it ends.
-//   k_lora_prep  : Q8_0 of x, and a counting sort of the tokens by adapter;
+//   k_lora_prep  : the operands of the base product, and a counting sort of the
+//                  tokens by adapter;
 //   k_lora_shrink: scale A x, 16 tokens of one adapter per cluster (tf32 hi + lo);
-//   k_lora_gemm  : the base product, tiles of W rows by tokens;
+//   k_lora_base  : the base product;
 //   k_lora_expand: adds B (scale A x), 16 tokens of one adapter per CTA.
 #include <cooperative_groups.h>
 
 #include "moe_lora.cuh"
+#include "moe_umma.cuh"
 
 namespace moe {
 namespace {
 
-// Scales and starting values of tokens 2i and 2i + 1 for group g, kXs words at
-// xs + (i * G + g) * kXs: d of block 0 for the two tokens, d of block 1, then
-// block 0's starting values c as the MMA's four accumulators take them
-// (c, c', c, c'), and block 1's.
+// Scales and starting values of tokens 2i and 2i + 1 for group g: kXs words at
+// xs + (i * G + g) * kXs -- d of block 0 for the two tokens, d of block 1,
+// block 0's starting values, block 1's.
 __device__ __forceinline__ void store_xs(float *xs, int t, int G, int k, float d, int c) {
   float *p = xs + ((int64_t)(t >> 1) * G + (k >> 6)) * kXs + (t & 1);
   const int b = (k >> 5) & 1;
   p[2 * b] = d;
-  p[4 + 4 * b] = __int_as_float(c);
-  p[6 + 4 * b] = __int_as_float(c);
+  p[4 + 2 * b] = __int_as_float(c);
 }
 
-// Q8_0 of four elements (8 lanes share a 32-block): the codes packed, and for
-// the block's first lane its scale and starting value.  The scale is the
+// Q8_0 of four elements (8 lanes share a 32-block) and the block's scale.  The scale is the
 // product with fp32's 1/127, as tensor libraries evaluate a division by a
 // constant: at most a unit in the last place from amax / 127.
-__device__ __forceinline__ uint32_t quant4(const float4 v, float &d, int &c) {
+__device__ __forceinline__ int4 quant4(const float4 v, float &d) {
   float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
   for (int off = 4; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   d = fmul(m, 1.0f / 127.0f);
-  const int q0 = q8_code(v.x, d), q1 = q8_code(v.y, d), q2 = q8_code(v.z, d), q3 = q8_code(v.w, d);
-  int s = q0 + q1 + q2 + q3;
-#pragma unroll
-  for (int off = 4; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  c = kMagicBits - 8 * s;
-  return (uint32_t)(q0 & 255) | ((uint32_t)(q1 & 255) << 8) | ((uint32_t)(q2 & 255) << 16) | ((uint32_t)q3 << 24);
+  return make_int4(q8_code(v.x, d), q8_code(v.y, d), q8_code(v.z, d), q8_code(v.w, d));
 }
 
 // ===========================================================================
@@ -77,16 +64,20 @@ __global__ void __launch_bounds__(128) k_lora_in(const LoraArgs a) {
   const int t = blockIdx.y, k0 = blockIdx.x * kLoraSlice;
   const int G = a.K / 64, r = a.r;
   pdl_launch_dependents();
+  if (blockIdx.x == 0 && t == 0 && tid < 4) a.status[tid] = 0;
   const int k = k0 + 4 * tid;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (k < a.K) v = *reinterpret_cast<const float4 *>(a.x + (size_t)t * a.K + k);
   const int id = adapter_of(a, t);
   float d;
-  int c;
-  const uint32_t q = quant4(v, d, c);
+  const int4 q = quant4(v, d);
+  int sum = q.x + q.y + q.z + q.w;
+#pragma unroll
+  for (int off = 4; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   if (k < a.K) {
-    *reinterpret_cast<uint32_t *>(a.xq + (size_t)t * a.K + k) = q;
-    if ((tid & 7) == 0) store_xs(a.xs, t, G, k, d, c);
+    *reinterpret_cast<char4 *>(a.xq + (size_t)t * a.K + k) =
+        make_char4((signed char)q.x, (signed char)q.y, (signed char)q.z, (signed char)q.w);
+    if ((tid & 7) == 0) store_xs(a.xs, t, G, k, d, kMagicBits - 8 * sum);
   }
   if (id == a.n) return;
   *reinterpret_cast<float4 *>(xsm + 4 * tid) = v;
@@ -131,10 +122,10 @@ __device__ __forceinline__ NibblePair nibbles(const uint2 l, const uint2 h) {
 
 // Accumulates one 64-group of a 16-row tile against eight columns.
 __device__ __forceinline__ void group_mma(f32x2 (&acc)[2], const NibblePair &w, const uint2 b0, const uint2 b1,
-                                          const float4 d, const float4 c0, const float4 c1, f32x2 s0, f32x2 s1) {
+                                          const float4 d, const float4 c, f32x2 s0, f32x2 s1) {
   int p[4], q[4];
-  mma_u8s8(p, w.lo, b0, c0);
-  mma_u8s8(q, w.hi, b1, c1);
+  mma_u8s8(p, w.lo, b0, c.x, c.y);
+  mma_u8s8(q, w.hi, b1, c.z, c.w);
   const f32x2 m = pack2(-kMagic, -kMagic);
   const f32x2 d0 = pack2(d.x, d.y), d1 = pack2(d.z, d.w);
   const f32x2 tl = fma2(add2(pack2i(q[0], q[1]), m), d1, mul2(add2(pack2i(p[0], p[1]), m), d0));
@@ -193,7 +184,7 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
           const int8_t *cq = a.xq + (size_t)(j * 8 + gq) * a.K + (size_t)g * 64 + q4 * 8;
           const uint2 b0 = *reinterpret_cast<const uint2 *>(cq), b1 = *reinterpret_cast<const uint2 *>(cq + 32);
           const float4 *x4 = reinterpret_cast<const float4 *>(a.xs + ((size_t)(j * 4 + q4) * G + g) * kXs);
-          group_mma(acc[j], w, b0, b1, x4[0], x4[1], x4[2], p0, p1);
+          group_mma(acc[j], w, b0, b1, x4[0], x4[1], p0, p1);
         }
       }
     }
@@ -315,8 +306,9 @@ __device__ void sort_tokens(const LoraArgs &a, int *tab, int warps) {
 }
 
 // The first kernel of a sorted call.  CTA 0 sorts the tokens by adapter; the
-// others (where `quant`) take the Q8_0 codes of x, a warp four times 128
-// inputs of a token at once.
+// others (where `operands`) lay out the base product's operands, all exact in
+// fp16: the Q8_0 codes of x (a warp: 512 inputs of a token), W's integers (a
+// warp: 1024 packed bytes), and in fp32 the scales of both, transposed.
 __global__ void __launch_bounds__(1024) k_lora_prep(const LoraArgs a, int warps) {
   extern __shared__ int tab[];  // [warps][n + 1]
   pdl_launch_dependents();
@@ -326,23 +318,59 @@ __global__ void __launch_bounds__(1024) k_lora_prep(const LoraArgs a, int warps)
     return;
   }
   const int lane = threadIdx.x & 31, per = (a.K + 511) / 512, G = a.K / 64;
-  const int64_t n = (int64_t)a.T * per;
-  for (int64_t i = (int64_t)(blockIdx.x - 1) * 32 + (threadIdx.x >> 5); i < n; i += (int64_t)(gridDim.x - 1) * 32) {
-    const int t = (int)(i / per), k = (int)(i - (int64_t)t * per) * 512 + lane * 4;
-    float4 v[4];
+  const int Tp = (a.T + kLoraTile - 1) / kLoraTile * kLoraTile;
+  const int64_t wbytes = (int64_t)a.N * (a.K / 2);
+  const int64_t nx = (int64_t)a.T * per, nw = (wbytes + 1023) / 1024;
+  const int64_t ns = ((int64_t)a.N * G + 127) / 128;
+  for (int64_t i = (int64_t)(blockIdx.x - 1) * 32 + (threadIdx.x >> 5); i < nx + nw + ns;
+       i += (int64_t)(gridDim.x - 1) * 32) {
+    if (i < nx) {
+      const int t = (int)(i / per), k = (int)(i - (int64_t)t * per) * 512 + lane * 4;
+      float4 v[4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
-      v[m] = k + 128 * m < a.K ? __ldg(reinterpret_cast<const float4 *>(a.x + (size_t)t * a.K + k + 128 * m))
-                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int m = 0; m < 4; ++m)
+        v[m] = k + 128 * m < a.K ? __ldg(reinterpret_cast<const float4 *>(a.x + (size_t)t * a.K + k + 128 * m))
+                                 : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int km = k + 128 * m;
-      float d;
-      int c;
-      const uint32_t q = quant4(v[m], d, c);
-      if (km < a.K) {
-        *reinterpret_cast<uint32_t *>(a.xq + (size_t)t * a.K + km) = q;
-        if ((lane & 7) == 0) store_xs(a.xs, t, G, km, d, c);
+      for (int m = 0; m < 4; ++m) {
+        const int km = k + 128 * m;
+        float d;
+        const int4 q = quant4(v[m], d);
+        if (km < a.K) {
+          const __half2 h0 = __halves2half2(__int2half_rn(q.x), __int2half_rn(q.y));
+          const __half2 h1 = __halves2half2(__int2half_rn(q.z), __int2half_rn(q.w));
+          *reinterpret_cast<uint2 *>(a.xh + (size_t)t * a.K + km) =
+              make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+          if ((lane & 7) == 0) a.xd[((size_t)(km >> 6) * Tp + t) * 2 + ((km >> 5) & 1)] = d;
+        }
+      }
+    } else if (i < nx + nw) {
+      // bytes o .. o + 7 of a 32-byte group: 8 values of its block 0, 8 of its block 1
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int64_t o = (i - nx) * 1024 + m * 256 + lane * 8;
+        if (o < wbytes) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2 *>(a.W + o));
+          uint4 lo, hi;
+          nib4_to_f16(w.x & 0x0F0F0F0Fu, lo.x, lo.y);
+          nib4_to_f16(w.y & 0x0F0F0F0Fu, lo.z, lo.w);
+          nib4_to_f16((w.x >> 4) & 0x0F0F0F0Fu, hi.x, hi.y);
+          nib4_to_f16((w.y >> 4) & 0x0F0F0F0Fu, hi.z, hi.w);
+          __half *dst = a.wh + (o >> 5) * 64 + (o & 31);
+          *reinterpret_cast<uint4 *>(dst) = lo;
+          *reinterpret_cast<uint4 *>(dst + 32) = hi;
+        }
+      }
+    } else {
+      // scales: element e = (g, n), n fastest
+      const __half *sc = reinterpret_cast<const __half *>(a.W + wbytes);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const int64_t e = (i - nx - nw) * 128 + m * 32 + lane;
+        if (e < (int64_t)a.N * G) {
+          const int g = (int)(e / a.N), n = (int)(e - (int64_t)g * a.N);
+          a.ws[(size_t)g * a.Nt + n] = __half2float(__ldg(sc + (size_t)n * G + g));
+        }
       }
     }
   }
@@ -521,153 +549,216 @@ __global__ void __launch_bounds__(256) k_lora_shrink(const LoraArgs a, const flo
   cluster.sync();  // the shares stay until they have been read
 }
 
-// Tiles of BM rows of W by BN tokens, in token order.  Stages of two 64-groups
-// come through shared memory by cp.async; with KW = 2 one half of the warps
-// takes the first group of a stage and the other half the second, joined at
-// the end.  Row strides of 96 (weights) and 160 (codes) bytes keep the
-// fragments' 8-byte reads free of bank conflicts.
+// The base product on the fifth-generation tensor cores: tiles of 128 tokens
+// (TMEM lanes) by BN rows of W (columns), in token order.  Codes and weights are
+// integers, exact in fp16, and a block of 32 of them (two MMAs of 16) sums to an
+// exact integer in the fp32 accumulator, so the only roundings are those of
+//   acc += s (S_0 d_0 + S_1 d_1)
+// per 64-group, in packed fp32 by the warps that read the accumulators: a lane
+// holds a token (its d), the scales s come with the stage.  The arithmetic
+// sets the pace (three packed operations per two outputs and group, 768 clocks
+// per 64-group of a 128 x 256 tile; the MMAs take 512): that is why one exact
+// pass with two accumulators per group wins over fp16 hi + lo operands (two
+// passes, 1024 clocks).
+//
+// Warp 0 copies stages of one 64-group by TMA, warp 1 issues the MMAs, warps 2-9
+// take a quarter of the tokens by half of the columns.  The two column halves
+// have accumulators of their own (two blocks each, and SETS sets of them where
+// tensor memory has room), so that one half's MMAs run while the other's sums
+// are read.  With few tiles a cluster of CTAs splits K; their sums are joined in
+// the first one through distributed shared memory.  Every wait is bounded.
 //
 // The kernel reads nothing of the launch right before it (k_lora_shrink; that
 // one starts it after its own wait for k_lora_prep), so it runs beside it, and
 // waits for it only before it ends: k_lora_expand, which waits for this
 // kernel, then has both results.
-template <int WM_, int WN_, int KW_, int MT_, int NT_, int STG_>
-struct GemmCfg {
-  static constexpr int WM = WM_, WN = WN_, KW = KW_, MT = MT_, NT = NT_, STG = STG_;
-  static constexpr int BM = WM * MT * 16, BN = WN * NT * 8, THREADS = WM * WN * KW * 32;
-  static constexpr int WB = BM * 96, CB = BN * 160, XB = BN * kXs * 4, STAGE = WB + CB + XB;
-  static size_t smem(int G) {
-    const size_t main = (size_t)STG * STAGE + ((size_t)BM * G * 2 + 15) / 16 * 16;
-    const size_t join = KW > 1 ? (size_t)(KW - 1) * BM * BN * 4 : 0;
-    return main > join ? main : join;
-  }
+template <int BN_, int STG_>
+struct BaseCfg {
+  static constexpr int BN = BN_, STG = STG_, HN = BN / 2;   // columns per tile and per half
+  static constexpr int SETS = 512 / (4 * HN) < 2 ? 1 : 2;   // sets of (half, block) accumulators
+  static constexpr uint32_t AB = 128 * 128, BB = BN * 128, SB = BN * 4, STAGE = AB + BB + SB;
+  static constexpr uint32_t COLS = SETS * 4 * HN;
+  static constexpr size_t SMEM = 1024 + 1024 + (size_t)STG * (AB + BB) + (size_t)STG * SB;
+  static_assert((size_t)128 * (BN + 4) * 4 <= (size_t)STG * (AB + BB) || BN > 128, "the join fits the stages");
 };
 
 template <typename C>
-__global__ void __launch_bounds__(C::THREADS) k_lora_gemm(const LoraArgs a) {
-  extern __shared__ __align__(128) unsigned char gsm[];
-  constexpr int BM = C::BM, BN = C::BN, MT = C::MT, NT = C::NT;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, q4 = lane & 3;
-  const int G = a.K / 64, N = a.N, T = a.T;
-  const int wm = warp % C::WM, wn = warp / C::WM % C::WN, kw = warp / (C::WM * C::WN);
-  const int n0 = blockIdx.x * BM, p0 = blockIdx.y * BN;
-  const __half *ssc = reinterpret_cast<const __half *>(gsm + C::STG * C::STAGE);  // [BM][G]
-  const int S = (G + 1) / 2;
-  auto load_stage = [&](int st) {
-    unsigned char *b = gsm + (st % C::STG) * C::STAGE;
-    const int g0 = 2 * st, ng = min(2, G - g0);
-    for (int i = tid; i < BM * 4; i += C::THREADS) {
-      const int row = i >> 2, c = i & 3;
-      if (c < 2 * ng)
-        cp_async16(b + row * 96 + c * 16, a.W + (size_t)min(n0 + row, N - 1) * (a.K / 2) + (size_t)g0 * 32 + c * 16);
+__global__ void __launch_bounds__(320, 1) k_lora_base(const LoraArgs a, const __grid_constant__ CUtensorMap xmap,
+                                                      const __grid_constant__ CUtensorMap wmap) {
+  extern __shared__ unsigned char bsm_raw[];
+  unsigned char *bsm = bsm_raw + (1024 - (smem_u32(bsm_raw) & 1023)) % 1024;
+  namespace cg = cooperative_groups;
+  constexpr int BN = C::BN, HN = C::HN, STG = C::STG, SETS = C::SETS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t *full = reinterpret_cast<uint64_t *>(bsm), *empty = full + STG;
+  uint64_t *accfull = empty + STG, *accfree = accfull + 2 * SETS, *done = accfree + 2 * SETS;  // [set][half]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  unsigned char *buf = bsm + 1024;                                       // [STG][A, B]
+  float *sbuf = reinterpret_cast<float *>(buf + STG * (C::AB + C::BB));  // [STG][BN]
+  const int n0 = blockIdx.x * BN, t0 = blockIdx.y * 128, G = a.K / 64;
+  const int shares = (int)gridDim.z, share = (int)blockIdx.z;
+  const int g0 = (int)((int64_t)G * share / shares), S = (int)((int64_t)G * (share + 1) / shares) - g0;
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    for (int s = 0; s < STG; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1 + 8);  // the MMAs have read A and B, eight warps the scales
     }
-    for (int i = tid; i < BN * 8; i += C::THREADS) {
-      const int row = i >> 3, c = i & 7;
-      if (c < 4 * ng)
-        cp_async16(b + C::WB + row * 160 + c * 16, a.xq + (size_t)(p0 + row) * a.K + (size_t)g0 * 64 + c * 16);
+    for (int s = 0; s < 2 * SETS; ++s) {
+      mbar_init(accfull + s, 1);
+      mbar_init(accfree + s, 4);
     }
-    // per pair of tokens kXs / 4 pieces for each group: [group][pair][kXs]
-    for (int i = tid; i < BN * (kXs / 4); i += C::THREADS) {
-      const int pr = i / (2 * (kXs / 4)), c = i - pr * (2 * (kXs / 4)), gg = c / (kXs / 4), cc = c - gg * (kXs / 4);
-      if (gg < ng)
-        cp_async16(b + C::WB + C::CB + (gg * (BN / 2) + pr) * (kXs * 4) + cc * 16,
-                   a.xs + ((size_t)(p0 / 2 + pr) * G + g0 + gg) * kXs + cc * 4);
-    }
-  };
-  {
-    // the scales of the tile's rows, one run of bytes (n0 G 2 is a multiple of 16)
-    const unsigned char *sc = a.W + (size_t)N * (a.K / 2) + (size_t)n0 * G * 2;
-    const int bytes = min(BM, N - n0) * G * 2;  // N % 8 == 0: a multiple of 16
-    for (int i = tid; i < bytes / 16; i += C::THREADS) cp_async16(gsm + C::STG * C::STAGE + i * 16, sc + i * 16);
+    mbar_init(done, 1);
+    fence_barrier_init();
   }
-#pragma unroll
-  for (int st = 0; st < C::STG - 1; ++st) {
-    if (st < S) load_stage(st);
-    cp_async_commit();
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, C::COLS);
+    tmem_relinquish();
   }
-  f32x2 acc[MT][NT][2];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j][0] = acc[i][j][1] = 0ull;
-
-  for (int st = 0; st < S; ++st) {
-    cp_async_wait<C::STG - 2>();
-    __syncthreads();
-    if (st + C::STG - 1 < S) load_stage(st + C::STG - 1);
-    cp_async_commit();
-    const unsigned char *b = gsm + (st % C::STG) * C::STAGE;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (C::KW == 2 && h != kw) continue;
-      const int g = 2 * st + h;
-      if (g >= G) break;
-      NibblePair w[MT];
-      f32x2 s0[MT], s1[MT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int row = (wm * MT + i) * 16 + gq;
-        w[i] = nibbles(*reinterpret_cast<const uint2 *>(b + row * 96 + h * 32 + q4 * 8),
-                       *reinterpret_cast<const uint2 *>(b + (row + 8) * 96 + h * 32 + q4 * 8));
-        const float e = __half2float(ssc[row * G + g]), f = __half2float(ssc[(row + 8) * G + g]);
-        s0[i] = pack2(e, e);
-        s1[i] = pack2(f, f);
-      }
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int col = (wn * NT + j) * 8;
-        const unsigned char *cb = b + C::WB + (col + gq) * 160 + h * 64 + q4 * 8;
-        const uint2 b0 = *reinterpret_cast<const uint2 *>(cb), b1 = *reinterpret_cast<const uint2 *>(cb + 32);
-        const float4 *x4 = reinterpret_cast<const float4 *>(b + C::WB + C::CB + (h * (BN / 2) + col / 2 + q4) * (kXs * 4));
-        const float4 d = x4[0], c0 = x4[1], c1 = x4[2];
-#pragma unroll
-        for (int i = 0; i < MT; ++i) group_mma(acc[i][j], w[i], b0, b1, d, c0, c1, s0[i], s1[i]);
-      }
-    }
-  }
-  cp_async_wait<0>();
-  if (C::KW == 2) {
-    // the second half's sums go to the first through shared memory
-    __syncthreads();
-    f32x2 *join = reinterpret_cast<f32x2 *>(gsm) + (size_t)(warp % (C::WM * C::WN)) * (MT * NT * 2 * 32) + lane;
-    if (kw == 1) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          join[((i * NT + j) * 2) * 32] = acc[i][j][0];
-          join[((i * NT + j) * 2 + 1) * 32] = acc[i][j][1];
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  f32x2 acc[HN / 2];
+  const int q = warp & 3, half = (warp - 2) >> 2;  // epilogue warps: TMEM lane quarter, column half
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int j = 0; j < S; ++j) {
+        const int s = j % STG;
+        if (j >= STG && !mbar_wait(empty + s, (uint32_t)(j / STG - 1) & 1u, a.status, kDetLoraGemmEmpty, a.wait_limit)) {
+          *abort_flag = 1;
+          break;
         }
+        unsigned char *b = buf + s * (C::AB + C::BB);
+        mbar_arrive_expect_tx(full + s, C::STAGE);
+        tma_load_2d(b, &xmap, (g0 + j) * 64, t0, full + s);
+        tma_load_2d(b + C::AB, &wmap, (g0 + j) * 64, n0, full + s);
+        bulk_g2s(sbuf + s * BN, a.ws + (size_t)(g0 + j) * a.Nt + n0, C::SB, full + s);
+        issued = j + 1;
+        if (*abort_flag) break;
+      }
+      for (int j = max(0, issued - STG); j < issued; ++j)
+        mbar_drain(full + j % STG, (uint32_t)(j / STG) & 1u, a.status, kDetLoraGemmDrain);
     }
-    __syncthreads();
-    if (kw == 0) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          acc[i][j][0] = add2(acc[i][j][0], join[((i * NT + j) * 2) * 32]);
-          acc[i][j][1] = add2(acc[i][j][1], join[((i * NT + j) * 2 + 1) * 32]);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = pf_idesc(HN);
+      bool bad = false;
+      for (int j = 0; j < S && !bad; ++j) {
+        const int s = j % STG, set = j % SETS;
+        if (!mbar_wait(full + s, (uint32_t)(j / STG) & 1u, a.status, kDetLoraGemmFull, a.wait_limit) || *abort_flag) {
+          bad = true;
+          break;
         }
-    }
-  }
-  if (kw == 0) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int t = p0 + (wn * NT + j) * 8 + 2 * q4 + c;
-        if (t < T) {
-          float *row = a.out + (size_t)t * N;
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            const int n = n0 + (wm * MT + i) * 16 + gq;
-            const float2 x = unpack2(acc[i][j][0]), y = unpack2(acc[i][j][1]);
-            if (n < N) row[n] = c ? x.y : x.x;
-            if (n + 8 < N) row[n + 8] = c ? y.y : y.x;
+        const uint64_t ad = umma_desc_sw128(smem_u32(buf + s * (C::AB + C::BB)));
+        const uint64_t bd = umma_desc_sw128(smem_u32(buf + s * (C::AB + C::BB) + C::AB));
+        for (int h = 0; h < 2; ++h) {
+          if (j >= SETS && !mbar_wait(accfree + 2 * set + h, (uint32_t)(j / SETS - 1) & 1u, a.status, kDetLoraFree,
+                                      a.wait_limit)) {
+            bad = true;
+            break;
           }
+          tc_fence_after();
+          const uint32_t d = tmem + (uint32_t)((2 * set + h) * 2 * HN);
+          const uint64_t bh = bd + (uint64_t)((h * HN * 128) >> 4);
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const uint64_t o = (uint64_t)((b * 64) >> 4);
+            umma_f16(d + (uint32_t)(b * HN), ad + o, bh + o, idesc, 0u);
+            umma_f16(d + (uint32_t)(b * HN), ad + o + 2, bh + o + 2, idesc, 1u);
+          }
+          umma_commit(accfull + 2 * set + h);
+        }
+        if (!bad) umma_commit(empty + s);
+      }
+      if (bad) *abort_flag = 1;
+      umma_commit(done);
+      mbar_drain(done, 0, a.status, kDetLoraGemmDrain);
+    }
+    __syncwarp();
+  } else {
+#pragma unroll
+    for (int i = 0; i < HN / 2; ++i) acc[i] = 0ull;
+    const int Tp = (a.T + kLoraTile - 1) / kLoraTile * kLoraTile;
+    const float2 *xd = reinterpret_cast<const float2 *>(a.xd) + (size_t)g0 * Tp + t0 + q * 32 + lane;
+    const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 2 * HN);
+    float2 dn = S > 0 ? xd[0] : make_float2(0.0f, 0.0f);
+    for (int j = 0; j < S; ++j) {
+      const int s = j % STG, set = j % SETS;
+      const float2 d = dn;
+      if (j + 1 < S) dn = xd[(size_t)(j + 1) * Tp];
+      // (the stage's scales landed with what the MMAs waited for)
+      const bool got = mbar_wait(accfull + 2 * set + half, (uint32_t)(j / SETS) & 1u, a.status, kDetLoraAcc, a.wait_limit);
+      if (!__all_sync(0xffffffffu, got && *abort_flag == 0)) {
+        *abort_flag = 1;
+        break;
+      }
+      mbar_try_wait(full + s, (uint32_t)(j / STG) & 1u);  // complete: orders the copied scales before the reads below
+      tc_fence_after();
+      const f32x2 d0 = pack2(d.x, d.x), d1 = pack2(d.y, d.y);
+      const float2 *sc = reinterpret_cast<const float2 *>(sbuf + s * BN + half * HN);
+      const uint32_t ta = at + (uint32_t)(set * 4 * HN);
+      // eight columns at a time (128 sums stay in registers)
+#pragma unroll
+      for (int c = 0; c < HN; c += 8) {
+        uint32_t v0[8], v1[8];
+        tmem_ld8(ta + (uint32_t)c, v0);
+        tmem_ld8(ta + (uint32_t)(HN + c), v1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const float2 sv = sc[(c + i) / 2];
+          const f32x2 p = mul2(pack2i(v0[i], v0[i + 1]), d0);
+          acc[(c + i) / 2] = fma2(fma2(pack2i(v1[i], v1[i + 1]), d1, p), pack2(sv.x, sv.y), acc[(c + i) / 2]);
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(accfree + 2 * set + half);
+        mbar_arrive(empty + s);
+      }
     }
+  }
+  // every copy and MMA of this CTA has completed (warps 0 and 1 waited for them)
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::COLS);
+  }
+  bool ok = *abort_flag == 0;
+  if (shares > 1) {
+    // rows of BN + 4 words, so that the lanes' 16-byte accesses spread over the banks
+    cg::cluster_group cluster = cg::this_cluster();
+    float *mine = reinterpret_cast<float *>(buf);
+    const int row = q * 32 + lane;
+    if (warp >= 2 && share > 0)
+#pragma unroll
+      for (int i = 0; i < HN; i += 4)
+        *reinterpret_cast<ulonglong2 *>(mine + row * (BN + 4) + half * HN + i) = make_ulonglong2(acc[i / 2], acc[i / 2 + 1]);
+    cluster.sync();
+    if (warp >= 2 && share == 0)
+      for (int c = 1; c < shares; ++c) {
+        const float *r = cluster.map_shared_rank(mine, c) + row * (BN + 4) + half * HN;
+#pragma unroll
+        for (int i = 0; i < HN; i += 4) {
+          const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(r + i);
+          acc[i / 2] = add2(acc[i / 2], v.x);
+          acc[i / 2 + 1] = add2(acc[i / 2 + 1], v.y);
+        }
+      }
+    cluster.sync();  // the shares stay until they have been read
+  }
+  const int t = t0 + q * 32 + lane, nc = n0 + half * HN;
+  if (warp >= 2 && share == 0 && ok && t < a.T) {
+    float *row = a.out + (size_t)t * a.N + nc;
+#pragma unroll
+    for (int i = 0; i < HN; i += 4)
+      if (nc + i < a.N) *reinterpret_cast<ulonglong2 *>(row + i) = make_ulonglong2(acc[i / 2], acc[i / 2 + 1]);
   }
   pdl_launch_dependents();
   pdl_wait();
@@ -853,27 +944,40 @@ cudaError_t small(const LoraArgs &a, cudaStream_t s) {
 }
 
 template <typename C>
-cudaError_t gemm(const LoraArgs &a, bool pdl, cudaStream_t s) {
-  const size_t smem = C::smem(a.K / 64);
+cudaError_t base(const LoraArgs &a, int shares, bool pdl, cudaStream_t s) {
   static int smem_set[64] = {0};
-  cudaError_t err = ensure_smem(k_lora_gemm<C>, smem, smem_set);
+  cudaError_t err = ensure_smem(k_lora_base<C>, C::SMEM, smem_set);
+  CUtensorMap xmap, wmap;
+  if (err == cudaSuccess) err = make_f16_map(&xmap, a.xh, (uint64_t)a.T, (uint64_t)a.K, 128);
+  if (err == cudaSuccess) err = make_f16_map(&wmap, a.wh, (uint64_t)a.N, (uint64_t)a.K, C::BN);
   if (err != cudaSuccess) return err;
-  const dim3 grid((unsigned)((a.N + C::BM - 1) / C::BM), (unsigned)((a.T + C::BN - 1) / C::BN));
-  if (pdl) return launch_pdl(k_lora_gemm<C>, grid, dim3(C::THREADS), smem, s, a);
-  k_lora_gemm<C><<<grid, C::THREADS, smem, s>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((a.N + C::BN - 1) / C::BN), (unsigned)((a.T + 127) / 128), (unsigned)shares);
+  cfg.blockDim = dim3(320);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = (unsigned)shares;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = pdl ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, k_lora_base<C>, a, xmap, wmap);
 }
 
 }  // namespace
 
-cudaError_t launch_lora_prep(const LoraArgs &a, bool quant, int sms, cudaStream_t s) {
+cudaError_t launch_lora_prep(const LoraArgs &a, bool operands, int sms, cudaStream_t s) {
   // tables of 32 warps where they fit, of 8 for thousands of adapters
   const int warps = a.n < 1024 ? 32 : 8;
   const size_t smem = (size_t)warps * (a.n + 1) * 4;
   static int smem_set[64] = {0};
   cudaError_t err = ensure_smem(k_lora_prep, smem, smem_set);
   if (err != cudaSuccess) return err;
-  int64_t ctas = quant ? ((int64_t)a.T * ((a.K + 511) / 512) + 31) / 32 : 0;
+  const int64_t units = (int64_t)a.T * ((a.K + 511) / 512) + (int64_t)a.N * a.K / 2048 + (int64_t)a.N * a.K / 8192;
+  int64_t ctas = operands ? units / 32 + 1 : 0;
   if (ctas > 2 * sms) ctas = 2 * sms;
   k_lora_prep<<<(unsigned)(1 + ctas), 1024, smem, s>>>(a, warps);
   return cudaGetLastError();
@@ -907,11 +1011,22 @@ cudaError_t launch_lora_large(const LoraArgs &a, int sms, cudaStream_t s) {
   const bool adapters = a.n > 0 || a.u != nullptr;  // without an adapter u is still written (zeros)
   if (err == cudaSuccess && adapters) err = launch_lora_shrink(a, a.x, a.K, a.A, false, a.us, a.u, sms, s);
   if (err != cudaSuccess) return err;
-  using Big = GemmCfg<2, 4, 1, 4, 4, 3>;    // 128 x 128
-  using Small = GemmCfg<2, 2, 2, 2, 4, 3>;  // 64 x 64, two halves of K
-  const int64_t tiles = (int64_t)((a.N + 127) / 128) * ((a.T + 127) / 128);
-  // without the shrink between them the GEMM follows the quantisation directly, and waits for it
-  err = tiles >= sms ? gemm<Big>(a, adapters, s) : gemm<Small>(a, adapters, s);
+  // 256 columns where the tiles fill most SMs once; else 128 or 64, and a
+  // split of K over a cluster while SMs are left and a share keeps eight groups
+  const int64_t rows = (a.T + 127) / 128, G = a.K / 64;
+  auto shares = [&](int64_t tiles) {
+    int c = 1;
+    while (c < 8 && tiles * c * 2 <= sms && G / (2 * c) >= 8) c *= 2;
+    return c;
+  };
+  // without the shrink between them the GEMM follows the layout directly, and waits for it
+  if (rows * ((a.N + 255) / 256) * 4 >= 3 * (int64_t)sms) {
+    err = base<BaseCfg<256, 4>>(a, 1, adapters, s);
+  } else if (rows * ((a.N + 127) / 128) * 2 >= sms) {
+    err = base<BaseCfg<128, 6>>(a, shares(rows * ((a.N + 127) / 128)), adapters, s);
+  } else {
+    err = base<BaseCfg<64, 8>>(a, shares(rows * ((a.N + 63) / 64)), adapters, s);
+  }
   if (err != cudaSuccess || a.n == 0) return err;
   return launch_lora_expand(a, a.us, a.B, true, a.N, a.out, s);
 }

@@ -67,14 +67,15 @@ __device__ __forceinline__ void add4(float (&d)[4], const float (&t)[4]) {
 }
 
 // ------------------------------------------------------------------ integer products
-// Block sums: D[16][8] = A[16][32] (unsigned bytes) B[32][8] (signed bytes) + C.
-// Lane 4 g + q holds bytes 4q .. 4q + 3 and 16 + 4q .. of rows g (a[0], a[2])
-// and g + 8 (a[1], a[3]) and of column g (b.x, b.y); C and D like a tf32 D.
-__device__ __forceinline__ void mma_u8s8(int (&d)[4], const uint32_t (&a)[4], const uint2 b, const float4 c) {
-  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+// Block sums: D[16][8] = A[16][32] (unsigned bytes) B[32][8] (signed bytes) + C,
+// C the same for every row (c0, c1: this lane's two columns, as bits).  Lane
+// 4 g + q holds bytes 4q .. 4q + 3 and 16 + 4q .. of rows g (a[0], a[2]) and
+// g + 8 (a[1], a[3]) and of column g (b.x, b.y); D like a tf32 D.
+__device__ __forceinline__ void mma_u8s8(int (&d)[4], const uint32_t (&a)[4], const uint2 b, float c0, float c1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};"
       : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "r"(__float_as_int(c.x)),
-        "r"(__float_as_int(c.y)), "r"(__float_as_int(c.z)), "r"(__float_as_int(c.w)));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b.x), "r"(b.y), "r"(__float_as_int(c0)),
+        "r"(__float_as_int(c1)));
 }
 // The sums leave the MMA as floats: started from the bit pattern of
 // 1.5 * 2^23, an integer of magnitude below 2^22 added to it is the float

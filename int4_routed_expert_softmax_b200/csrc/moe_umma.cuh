@@ -98,4 +98,17 @@ __device__ __forceinline__ uint32_t pf_idesc(int n) {
   return (1u << 4) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
+// Four offset-binary nibbles (one per byte, 0..15) -> four fp16 values u - 8.
+__device__ __forceinline__ void nib4_to_f16(uint32_t n, uint32_t &lo, uint32_t &hi) {
+  const uint32_t a = __byte_perm(n, 0x64646464u, 0x4140);  // halves 1024 + u0, 1024 + u1
+  const uint32_t b = __byte_perm(n, 0x64646464u, 0x4342);  // halves 1024 + u2, 1024 + u3
+  const __half2 c = __halves2half2(__ushort_as_half((unsigned short)0x6408), __ushort_as_half((unsigned short)0x6408));
+  __half2 ha = *reinterpret_cast<const __half2 *>(&a);
+  __half2 hb = *reinterpret_cast<const __half2 *>(&b);
+  ha = __hsub2(ha, c);
+  hb = __hsub2(hb, c);
+  lo = *reinterpret_cast<const uint32_t *>(&ha);
+  hi = *reinterpret_cast<const uint32_t *>(&hb);
+}
+
 }  // namespace moe
