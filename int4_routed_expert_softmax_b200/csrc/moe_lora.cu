@@ -377,8 +377,8 @@ __global__ void __launch_bounds__(1024) k_lora_prep(const LoraArgs a, int warps)
 }
 
 // dst[p][j] = scale_a sum_k src[token][k] M_a(j, k): a cluster takes one tile
-// of up to 16 tokens of one adapter, each of its CTAs a share of k, its eight
-// warps the share's steps of 32.  A lane's four consecutive k serve two MMAs
+// of up to 16 tokens of one adapter by up to 8 RT of the rank, each of its CTAs
+// a share of k, its eight warps the share's steps of 32.  A lane's four consecutive k serve two MMAs
 // (their order inside a sum is free, as long as both operands agree).  M = A:
 // lane (g, q) reads A[8 j + g][4q ..]; M = B (TR): the RT values j = g RT .. of
 // rows 4q .., so that the columns of MMA tile jt are j = RT g + jt.  The next
@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(1024) k_lora_prep(const LoraArgs a, int warps)
 template <int RT, bool TR>
 struct ShrinkStep {
   float4 x[2][2];               // [row half][16 of k]
-  uint32_t m[2][TR ? 4 * ((RT + 1) / 2) : 2 * RT];
+  uint32_t m[2][2 * RT];        // of each: the A or B values of a lane's four k
 };
 
 template <int RT, bool BF16, bool TR>
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(256) k_lora_shrink(const LoraArgs a, const flo
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int r = a.r, share = (int)cluster.block_rank(), shares = (int)cluster.num_blocks();
-  const int tile = (int)blockIdx.x / shares;
+  const int tile = (int)blockIdx.x / shares, j0 = (int)blockIdx.y * RT * 8, rb = min(r - j0, RT * 8);
   pdl_wait();
   pdl_launch_dependents();
   if (tile >= a.tile[a.n + 1]) return;  // one decision for the whole cluster
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(256) k_lora_shrink(const LoraArgs a, const flo
   const int p0 = a.off[id] + (tile - a.tile[id]) * kLoraSeg;
   const int np = min(kLoraSeg, a.off[id + 1] - p0);
   if (id == a.n) {
-    if (user != nullptr && share == 0)
+    if (user != nullptr && share == 0 && j0 == 0)
       for (int i = tid; i < np * r; i += 256) user[(size_t)a.perm[p0 + i / r] * r + i % r] = 0.0f;
     return;
   }
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(256) k_lora_shrink(const LoraArgs a, const flo
   const float *x0 = src + (size_t)a.perm[p0 + min(g, np - 1)] * L;
   const float *x1 = src + (size_t)a.perm[p0 + min(g + 8, np - 1)] * L;
   const bool in0 = g < np, in1 = g + 8 < np;
-  constexpr int RW = (RT + 1) / 2;  // TR: words of a lane's RT values of one row
+  constexpr int RW = RT / 2;  // TR: words of a lane's RT values of one row
   auto load = [&](ShrinkStep<RT, TR> &s, int k32) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -426,29 +426,20 @@ __global__ void __launch_bounds__(256) k_lora_shrink(const LoraArgs a, const flo
       if (TR) {
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
-          const uint16_t *row = Ma + (size_t)(k + m) * r + g * RT;
-          if (RT == 1) {
-            s.m[h][m] = in ? __ldg(row) : 0u;
-          } else if (RT == 2) {
-            s.m[h][m] = in && g * RT < r ? __ldg(reinterpret_cast<const uint32_t *>(row)) : 0u;
-          } else if (RT == 4) {
-            const uint2 v = in && g * RT < r ? __ldg(reinterpret_cast<const uint2 *>(row)) : make_uint2(0u, 0u);
-            s.m[h][2 * m] = v.x, s.m[h][2 * m + 1] = v.y;
+          const uint16_t *row = Ma + (size_t)(k + m) * r + j0 + g * RT;
+          const bool ok = in && g * RT < rb;
+          if (RT == 2) {
+            s.m[h][m] = ok ? __ldg(reinterpret_cast<const uint32_t *>(row)) : 0u;
           } else {
-#pragma unroll
-            for (int c = 0; c < RT / 8; ++c) {
-              const uint4 v = in && g * RT + 8 * c < r ? __ldg(reinterpret_cast<const uint4 *>(row) + c)
-                                                       : make_uint4(0u, 0u, 0u, 0u);
-              uint32_t *w = s.m[h] + m * RW + 4 * c;
-              w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-            }
+            const uint2 v = ok ? __ldg(reinterpret_cast<const uint2 *>(row)) : make_uint2(0u, 0u);
+            s.m[h][RW * m] = v.x, s.m[h][RW * m + RW - 1] = v.y;
           }
         }
       } else {
 #pragma unroll
         for (int j = 0; j < RT; ++j) {
-          const uint2 v = in && j * 8 < r ? __ldg(reinterpret_cast<const uint2 *>(Ma + (size_t)(j * 8 + g) * L + k))
-                                          : make_uint2(0u, 0u);
+          const uint2 v = in && j * 8 < rb ? __ldg(reinterpret_cast<const uint2 *>(Ma + (size_t)(j0 + j * 8 + g) * L + k))
+                                           : make_uint2(0u, 0u);
           s.m[h][2 * j] = v.x, s.m[h][2 * j + 1] = v.y;
         }
       }
@@ -498,23 +489,15 @@ __global__ void __launch_bounds__(256) k_lora_shrink(const LoraArgs a, const flo
   };
   const int steps = (L + 31) / 32, stride = 8 * shares;
   int st = share * 8 + warp;
-  if (RT <= 8) {
-    ShrinkStep<RT, TR> s[2];
-    if (st < steps) load(s[0], st * 32);
-    while (st < steps) {
+  ShrinkStep<RT, TR> s[2];
+  if (st < steps) load(s[0], st * 32);
+  while (st < steps) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if (st + stride < steps) load(s[b ^ 1], (st + stride) * 32);
-        compute(s[b]);
-        st += stride;
-        if (st >= steps) break;
-      }
-    }
-  } else {  // two steps would not fit in the registers
-    ShrinkStep<RT, TR> s;
-    for (; st < steps; st += stride) {
-      load(s, st * 32);
-      compute(s);
+    for (int b = 0; b < 2; ++b) {
+      if (st + stride < steps) load(s[b ^ 1], (st + stride) * 32);
+      compute(s[b]);
+      st += stride;
+      if (st >= steps) break;
     }
   }
   // column c of tile j: rank index 8 j + c, or RT c + j
@@ -538,12 +521,12 @@ __global__ void __launch_bounds__(256) k_lora_shrink(const LoraArgs a, const flo
   cluster.sync();
   if (share == 0) {
     const float sc = a.scale[id];
-    for (int i = tid; i < np * r; i += 256) {
-      const int p = i / r, j = i - p * r;
+    for (int i = tid; i < np * rb; i += 256) {
+      const int p = i / rb, j = i - p * rb;
       float s = 0.0f;
       for (int c = 0; c < shares; ++c) s += cluster.map_shared_rank(red, c)[p * RT * 8 + j];
-      dst[(size_t)(p0 + p) * r + j] = sc * s;
-      if (user != nullptr) user[(size_t)a.perm[p0 + p] * r + j] = s;
+      dst[(size_t)(p0 + p) * r + j0 + j] = sc * s;
+      if (user != nullptr) user[(size_t)a.perm[p0 + p] * r + j0 + j] = s;
     }
   }
   cluster.sync();  // the shares stay until they have been read
@@ -561,12 +544,14 @@ __global__ void __launch_bounds__(256) k_lora_shrink(const LoraArgs a, const flo
 // pass with two accumulators per group wins over fp16 hi + lo operands (two
 // passes, 1024 clocks).
 //
-// Warp 0 copies stages of one 64-group by TMA, warp 1 issues the MMAs, warps 2-9
-// take a quarter of the tokens by half of the columns.  The two column halves
-// have accumulators of their own (two blocks each, and SETS sets of them where
-// tensor memory has room), so that one half's MMAs run while the other's sums
-// are read.  With few tiles a cluster of CTAs splits K; their sums are joined in
-// the first one through distributed shared memory.  Every wait is bounded.
+// Eight warps take a quarter of the tokens by half of the columns each (sixteen
+// by a quarter: 1.07 us per group of a 128 x 256 tile against 0.94); warp 8
+// copies stages of one 64-group by TMA, warp 9 issues the MMAs.  The
+// two column halves have accumulators of their own (two blocks each, and SETS
+// sets of them where tensor memory has room), so that one half's MMAs run while
+// the other's sums are read.  With few tiles a cluster of CTAs splits K.  The
+// sums leave through shared memory, where each CTA of the cluster joins its
+// share of the columns in a fixed order.  Every wait is bounded.
 //
 // The kernel reads nothing of the launch right before it (k_lora_shrink; that
 // one starts it after its own wait for k_lora_prep), so it runs beside it, and
@@ -576,15 +561,23 @@ template <int BN_, int STG_>
 struct BaseCfg {
   static constexpr int BN = BN_, STG = STG_, HN = BN / 2;   // columns per tile and per half
   static constexpr int SETS = 512 / (4 * HN) < 2 ? 1 : 2;   // sets of (half, block) accumulators
-  static constexpr uint32_t AB = 128 * 128, BB = BN * 128, SB = BN * 4, STAGE = AB + BB + SB;
+  static constexpr uint32_t AB = 128 * 128, BB = BN * 128, SB = BN * 4, DB = 128 * 8, STAGE = AB + BB + SB + DB;
   static constexpr uint32_t COLS = SETS * 4 * HN;
-  static constexpr size_t SMEM = 1024 + 1024 + (size_t)STG * (AB + BB) + (size_t)STG * SB;
-  static_assert((size_t)128 * (BN + 4) * 4 <= (size_t)STG * (AB + BB) || BN > 128, "the join fits the stages");
+  static constexpr size_t SMEM = 1024 + 1024 + (size_t)STG * STAGE;  // alignment, barriers, stages
+  static_assert((size_t)128 * (BN + 4) * 4 <= (size_t)STG * (AB + BB), "the sums fit the stages");
 };
 
+// Launched at 168 registers a thread; the two epilogue warpgroups take 216, the
+// third (copies and MMAs) gives its own down to 72: 2 * 128 * 216 + 128 * 72 =
+// 384 * 168 (the host checks the launch count).
+constexpr int kBaseThreads = 384, kBaseLaunchRegs = 168, kBaseRegs = 216, kBaseRegsOther = 72;
+static_assert(2 * 128 * kBaseRegs + 128 * kBaseRegsOther <= kBaseThreads * kBaseLaunchRegs,
+              "register split exceeds the launch's registers");
+constexpr int kBaseTmaWarp = 8, kBaseMmaWarp = 9;
+
 template <typename C>
-__global__ void __launch_bounds__(320, 1) k_lora_base(const LoraArgs a, const __grid_constant__ CUtensorMap xmap,
-                                                      const __grid_constant__ CUtensorMap wmap) {
+__global__ void __launch_bounds__(kBaseThreads, 1) k_lora_base(const LoraArgs a, const __grid_constant__ CUtensorMap xmap,
+                                                               const __grid_constant__ CUtensorMap wmap) {
   extern __shared__ unsigned char bsm_raw[];
   unsigned char *bsm = bsm_raw + (1024 - (smem_u32(bsm_raw) & 1023)) % 1024;
   namespace cg = cooperative_groups;
@@ -595,7 +588,8 @@ __global__ void __launch_bounds__(320, 1) k_lora_base(const LoraArgs a, const __
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   unsigned char *buf = bsm + 1024;                                       // [STG][A, B]
-  float *sbuf = reinterpret_cast<float *>(buf + STG * (C::AB + C::BB));  // [STG][BN]
+  float *sbuf = reinterpret_cast<float *>(buf + STG * (C::AB + C::BB));  // [STG][BN] scales of W
+  float2 *dbuf = reinterpret_cast<float2 *>(sbuf + STG * BN);            // [STG][128] scales of the tokens' two blocks
   const int n0 = blockIdx.x * BN, t0 = blockIdx.y * 128, G = a.K / 64;
   const int shares = (int)gridDim.z, share = (int)blockIdx.z;
   const int g0 = (int)((int64_t)G * share / shares), S = (int)((int64_t)G * (share + 1) / shares) - g0;
@@ -603,7 +597,7 @@ __global__ void __launch_bounds__(320, 1) k_lora_base(const LoraArgs a, const __
     *abort_flag = 0;
     for (int s = 0; s < STG; ++s) {
       mbar_init(full + s, 1);
-      mbar_init(empty + s, 1 + 8);  // the MMAs have read A and B, eight warps the scales
+      mbar_init(empty + s, 8);  // a warp that has seen a half's MMAs done and read the scales
     }
     for (int s = 0; s < 2 * SETS; ++s) {
       mbar_init(accfull + s, 1);
@@ -612,7 +606,7 @@ __global__ void __launch_bounds__(320, 1) k_lora_base(const LoraArgs a, const __
     mbar_init(done, 1);
     fence_barrier_init();
   }
-  if (warp == 1) {
+  if (warp == kBaseMmaWarp) {
     tmem_alloc(tmem_slot, C::COLS);
     tmem_relinquish();
   }
@@ -620,146 +614,152 @@ __global__ void __launch_bounds__(320, 1) k_lora_base(const LoraArgs a, const __
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  f32x2 acc[HN / 2];
-  const int q = warp & 3, half = (warp - 2) >> 2;  // epilogue warps: TMEM lane quarter, column half
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kBaseRegsOther));
+    if (warp == kBaseTmaWarp) {
+      const int Tp = (a.T + kLoraTile - 1) / kLoraTile * kLoraTile;
       int issued = 0;
       for (int j = 0; j < S; ++j) {
         const int s = j % STG;
-        if (j >= STG && !mbar_wait(empty + s, (uint32_t)(j / STG - 1) & 1u, a.status, kDetLoraGemmEmpty, a.wait_limit)) {
+        if (j >= STG && !warp_wait(empty + s, (uint32_t)(j / STG - 1) & 1u, a.status, kDetLoraGemmEmpty, a.wait_limit)) {
           *abort_flag = 1;
           break;
         }
-        unsigned char *b = buf + s * (C::AB + C::BB);
-        mbar_arrive_expect_tx(full + s, C::STAGE);
-        tma_load_2d(b, &xmap, (g0 + j) * 64, t0, full + s);
-        tma_load_2d(b + C::AB, &wmap, (g0 + j) * 64, n0, full + s);
-        bulk_g2s(sbuf + s * BN, a.ws + (size_t)(g0 + j) * a.Nt + n0, C::SB, full + s);
+        if (elect_one()) {
+          unsigned char *b = buf + s * (C::AB + C::BB);
+          mbar_arrive_expect_tx(full + s, C::STAGE);
+          tma_load_2d(b, &xmap, (g0 + j) * 64, t0, full + s);
+          tma_load_2d(b + C::AB, &wmap, (g0 + j) * 64, n0, full + s);
+          bulk_g2s(sbuf + s * BN, a.ws + (size_t)(g0 + j) * a.Nt + n0, C::SB, full + s);
+          bulk_g2s(dbuf + s * 128, a.xd + ((size_t)(g0 + j) * Tp + t0) * 2, C::DB, full + s);
+        }
+        __syncwarp();
         issued = j + 1;
-        if (*abort_flag) break;
       }
       for (int j = max(0, issued - STG); j < issued; ++j)
         mbar_drain(full + j % STG, (uint32_t)(j / STG) & 1u, a.status, kDetLoraGemmDrain);
     }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
+    if (warp == kBaseMmaWarp) {
       const uint32_t idesc = pf_idesc(HN);
+      const uint64_t ad0 = umma_desc_sw128(smem_u32(buf));
       bool bad = false;
       for (int j = 0; j < S && !bad; ++j) {
         const int s = j % STG, set = j % SETS;
-        if (!mbar_wait(full + s, (uint32_t)(j / STG) & 1u, a.status, kDetLoraGemmFull, a.wait_limit) || *abort_flag) {
-          bad = true;
-          break;
-        }
-        const uint64_t ad = umma_desc_sw128(smem_u32(buf + s * (C::AB + C::BB)));
-        const uint64_t bd = umma_desc_sw128(smem_u32(buf + s * (C::AB + C::BB) + C::AB));
+        bad = !warp_wait(full + s, (uint32_t)(j / STG) & 1u, a.status, kDetLoraGemmFull, a.wait_limit);
+        const uint64_t ad = ad0 + (uint64_t)((s * (C::AB + C::BB)) >> 4);
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (j >= SETS && !mbar_wait(accfree + 2 * set + h, (uint32_t)(j / SETS - 1) & 1u, a.status, kDetLoraFree,
-                                      a.wait_limit)) {
-            bad = true;
-            break;
-          }
+          if (!bad && j >= SETS)
+            bad = !warp_wait(accfree + 2 * set + h, (uint32_t)(j / SETS - 1) & 1u, a.status, kDetLoraFree, a.wait_limit);
+          if (bad) break;
           tc_fence_after();
           const uint32_t d = tmem + (uint32_t)((2 * set + h) * 2 * HN);
-          const uint64_t bh = bd + (uint64_t)((h * HN * 128) >> 4);
+          const uint64_t bh = ad + (uint64_t)((C::AB + h * HN * 128) >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const uint64_t o = (uint64_t)((b * 64) >> 4);
-            umma_f16(d + (uint32_t)(b * HN), ad + o, bh + o, idesc, 0u);
-            umma_f16(d + (uint32_t)(b * HN), ad + o + 2, bh + o + 2, idesc, 1u);
+            for (int b = 0; b < 2; ++b) {
+              const uint64_t o = (uint64_t)((b * 64) >> 4);
+              umma_f16(d + (uint32_t)(b * HN), ad + o, bh + o, idesc, 0u);
+              umma_f16(d + (uint32_t)(b * HN), ad + o + 2, bh + o + 2, idesc, 1u);
+            }
+            umma_commit(accfull + 2 * set + h);
           }
-          umma_commit(accfull + 2 * set + h);
+          __syncwarp();
         }
-        if (!bad) umma_commit(empty + s);
       }
       if (bad) *abort_flag = 1;
-      umma_commit(done);
+      if (elect_one()) umma_commit(done);
+      __syncwarp();
       mbar_drain(done, 0, a.status, kDetLoraGemmDrain);
     }
     __syncwarp();
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kBaseRegs));
+    const int q = warp & 3, half = warp >> 2;  // TMEM lane quarter, column half
+    const int trow = q * 32 + lane;
+    f32x2 acc[HN / 2];
 #pragma unroll
     for (int i = 0; i < HN / 2; ++i) acc[i] = 0ull;
-    const int Tp = (a.T + kLoraTile - 1) / kLoraTile * kLoraTile;
-    const float2 *xd = reinterpret_cast<const float2 *>(a.xd) + (size_t)g0 * Tp + t0 + q * 32 + lane;
     const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 2 * HN);
-    float2 dn = S > 0 ? xd[0] : make_float2(0.0f, 0.0f);
     for (int j = 0; j < S; ++j) {
       const int s = j % STG, set = j % SETS;
-      const float2 d = dn;
-      if (j + 1 < S) dn = xd[(size_t)(j + 1) * Tp];
-      // (the stage's scales landed with what the MMAs waited for)
       const bool got = mbar_wait(accfull + 2 * set + half, (uint32_t)(j / SETS) & 1u, a.status, kDetLoraAcc, a.wait_limit);
-      if (!__all_sync(0xffffffffu, got && *abort_flag == 0)) {
+      if (!__all_sync(0xffffffffu, got)) {
         *abort_flag = 1;
         break;
       }
-      mbar_try_wait(full + s, (uint32_t)(j / STG) & 1u);  // complete: orders the copied scales before the reads below
       tc_fence_after();
-      const f32x2 d0 = pack2(d.x, d.x), d1 = pack2(d.y, d.y);
-      const float2 *sc = reinterpret_cast<const float2 *>(sbuf + s * BN + half * HN);
       const uint32_t ta = at + (uint32_t)(set * 4 * HN);
-      // eight columns at a time (128 sums stay in registers)
+      // 16 columns at a time, the next ones on their way out of tensor memory
+      // meanwhile (its wait covers every load issued so far)
+      uint32_t v0[2][16], v1[2][16];
+      tmem_ld16(ta, v0[0]);
+      tmem_ld16(ta + (uint32_t)HN, v1[0]);
+      // the stage's scales landed with what the MMAs waited for: this phase is
+      // complete, and testing it orders the copied bytes before the reads below
+      mbar_try_wait(full + s, (uint32_t)(j / STG) & 1u);
+      const float2 d = dbuf[s * 128 + trow];
+      const f32x2 d0 = pack2(d.x, d.x), d1 = pack2(d.y, d.y);
+      const float4 *sc = reinterpret_cast<const float4 *>(sbuf + s * BN + half * HN);
 #pragma unroll
-      for (int c = 0; c < HN; c += 8) {
-        uint32_t v0[8], v1[8];
-        tmem_ld8(ta + (uint32_t)c, v0);
-        tmem_ld8(ta + (uint32_t)(HN + c), v1);
+      for (int c = 0; c < HN; c += 16) {
+        const int b = (c >> 4) & 1;
         tmem_ld_wait();
+        if (c + 16 < HN) {
+          tmem_ld16(ta + (uint32_t)(c + 16), v0[b ^ 1]);
+          tmem_ld16(ta + (uint32_t)(HN + c + 16), v1[b ^ 1]);
+        } else {
+          // the accumulators are in registers: the MMAs may have them back
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(accfree + 2 * set + half);
+        }
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const float2 sv = sc[(c + i) / 2];
-          const f32x2 p = mul2(pack2i(v0[i], v0[i + 1]), d0);
-          acc[(c + i) / 2] = fma2(fma2(pack2i(v1[i], v1[i + 1]), d1, p), pack2(sv.x, sv.y), acc[(c + i) / 2]);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 sv = sc[(c + i) / 4];
+          const f32x2 p0 = mul2(pack2i(v0[b][i], v0[b][i + 1]), d0), p1 = mul2(pack2i(v0[b][i + 2], v0[b][i + 3]), d0);
+          f32x2 &a0 = acc[(c + i) / 2], &a1 = acc[(c + i) / 2 + 1];
+          a0 = fma2(fma2(pack2i(v1[b][i], v1[b][i + 1]), d1, p0), pack2(sv.x, sv.y), a0);
+          a1 = fma2(fma2(pack2i(v1[b][i + 2], v1[b][i + 3]), d1, p1), pack2(sv.z, sv.w), a1);
         }
       }
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(accfree + 2 * set + half);
-        mbar_arrive(empty + s);
-      }
+      if (lane == 0) mbar_arrive(empty + s);
     }
+    // the sums to shared memory, over the stages: their last copy and MMA are
+    // complete once all eight warps are here (rows of BN + 4 words spread the
+    // lanes' 16-byte accesses over the banks)
+    named_sync(1, 256);
+    float *mine = reinterpret_cast<float *>(buf) + trow * (BN + 4) + half * HN;
+#pragma unroll
+    for (int i = 0; i < HN; i += 4)
+      *reinterpret_cast<ulonglong2 *>(mine + i) = make_ulonglong2(acc[i / 2], acc[i / 2 + 1]);
   }
-  // every copy and MMA of this CTA has completed (warps 0 and 1 waited for them)
+  const bool ok = *abort_flag == 0;
+  cg::cluster_group cluster = cg::this_cluster();
   tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
+  if (shares > 1) cluster.sync();
+  else __syncthreads();
+  if (warp == kBaseMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::COLS);
   }
-  bool ok = *abort_flag == 0;
-  if (shares > 1) {
-    // rows of BN + 4 words, so that the lanes' 16-byte accesses spread over the banks
-    cg::cluster_group cluster = cg::this_cluster();
-    float *mine = reinterpret_cast<float *>(buf);
-    const int row = q * 32 + lane;
-    if (warp >= 2 && share > 0)
-#pragma unroll
-      for (int i = 0; i < HN; i += 4)
-        *reinterpret_cast<ulonglong2 *>(mine + row * (BN + 4) + half * HN + i) = make_ulonglong2(acc[i / 2], acc[i / 2 + 1]);
-    cluster.sync();
-    if (warp >= 2 && share == 0)
-      for (int c = 1; c < shares; ++c) {
-        const float *r = cluster.map_shared_rank(mine, c) + row * (BN + 4) + half * HN;
-#pragma unroll
-        for (int i = 0; i < HN; i += 4) {
-          const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(r + i);
-          acc[i / 2] = add2(acc[i / 2], v.x);
-          acc[i / 2 + 1] = add2(acc[i / 2 + 1], v.y);
-        }
+  if (ok) {
+    // this CTA's share of the columns, summed over the cluster
+    const int w4 = BN / 4 / shares, c0 = share * w4 * 4;
+    for (int i = threadIdx.x; i < 128 * w4; i += kBaseThreads) {
+      const int row = i / w4, c = c0 + (i - row * w4) * 4;
+      if (t0 + row >= a.T || n0 + c >= a.N) continue;
+      float *at = reinterpret_cast<float *>(buf) + row * (BN + 4) + c;
+      float4 v = *reinterpret_cast<const float4 *>(shares > 1 ? cluster.map_shared_rank(at, 0) : at);
+      for (int r = 1; r < shares; ++r) {
+        const float4 x = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(at, r));
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
       }
-    cluster.sync();  // the shares stay until they have been read
+      *reinterpret_cast<float4 *>(a.out + (size_t)(t0 + row) * a.N + n0 + c) = v;
+    }
   }
-  const int t = t0 + q * 32 + lane, nc = n0 + half * HN;
-  if (warp >= 2 && share == 0 && ok && t < a.T) {
-    float *row = a.out + (size_t)t * a.N + nc;
-#pragma unroll
-    for (int i = 0; i < HN; i += 4)
-      if (nc + i < a.N) *reinterpret_cast<ulonglong2 *>(row + i) = make_ulonglong2(acc[i / 2], acc[i / 2 + 1]);
-  }
+  if (shares > 1) cluster.sync();  // the sums stay until they have been read
   pdl_launch_dependents();
   pdl_wait();
 }
@@ -898,9 +898,9 @@ cudaError_t shrink(const LoraArgs &a, const float *src, int L, const void *M, fl
   cudaError_t err = ensure_smem(k_lora_shrink<RT, BF16, TR>, smem, smem_set);
   if (err != cudaSuccess) return err;
   const int tiles = lora_tiles(a);
-  const int shares = shrink_shares(tiles, L, sms);
+  const int shares = shrink_shares(tiles * ((a.r + RT * 8 - 1) / (RT * 8)), L, sms);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(tiles * shares));
+  cfg.gridDim = dim3((unsigned)(tiles * shares), (unsigned)((a.r + RT * 8 - 1) / (RT * 8)));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -918,10 +918,9 @@ cudaError_t shrink(const LoraArgs &a, const float *src, int L, const void *M, fl
 template <bool BF16, bool TR>
 cudaError_t shrink_rank(const LoraArgs &a, const float *src, int L, const void *M, float *dst, float *user, int sms,
                         cudaStream_t s) {
+  // blocks of 32 of the rank: with 64 a warp's registers leave one CTA per SM (59 us against TODO)
   if (a.r <= 16) return shrink<2, BF16, TR>(a, src, L, M, dst, user, sms, s);
-  if (a.r <= 32) return shrink<4, BF16, TR>(a, src, L, M, dst, user, sms, s);
-  if (a.r <= 64) return shrink<8, BF16, TR>(a, src, L, M, dst, user, sms, s);
-  return shrink<16, BF16, TR>(a, src, L, M, dst, user, sms, s);
+  return shrink<4, BF16, TR>(a, src, L, M, dst, user, sms, s);
 }
 
 template <int NT, bool BF16>
@@ -947,13 +946,15 @@ template <typename C>
 cudaError_t base(const LoraArgs &a, int shares, bool pdl, cudaStream_t s) {
   static int smem_set[64] = {0};
   cudaError_t err = ensure_smem(k_lora_base<C>, C::SMEM, smem_set);
+  static std::atomic<int> regs{0};
+  if (err == cudaSuccess) err = launch_regs_ok(k_lora_base<C>, kBaseLaunchRegs, regs);
   CUtensorMap xmap, wmap;
   if (err == cudaSuccess) err = make_f16_map(&xmap, a.xh, (uint64_t)a.T, (uint64_t)a.K, 128);
   if (err == cudaSuccess) err = make_f16_map(&wmap, a.wh, (uint64_t)a.N, (uint64_t)a.K, C::BN);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((a.N + C::BN - 1) / C::BN), (unsigned)((a.T + 127) / 128), (unsigned)shares);
-  cfg.blockDim = dim3(320);
+  cfg.blockDim = dim3(kBaseThreads);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute at[2] = {};
@@ -1011,22 +1012,15 @@ cudaError_t launch_lora_large(const LoraArgs &a, int sms, cudaStream_t s) {
   const bool adapters = a.n > 0 || a.u != nullptr;  // without an adapter u is still written (zeros)
   if (err == cudaSuccess && adapters) err = launch_lora_shrink(a, a.x, a.K, a.A, false, a.us, a.u, sms, s);
   if (err != cudaSuccess) return err;
-  // 256 columns where the tiles fill most SMs once; else 128 or 64, and a
-  // split of K over a cluster while SMs are left and a share keeps eight groups
-  const int64_t rows = (a.T + 127) / 128, G = a.K / 64;
-  auto shares = [&](int64_t tiles) {
-    int c = 1;
-    while (c < 8 && tiles * c * 2 <= sms && G / (2 * c) >= 8) c *= 2;
-    return c;
-  };
+  // Tiles of 256 columns, and a split of K over a cluster while SMs are left: a
+  // 64-group costs a CTA nearly the same for 64 columns as for 256 (what its
+  // warps hand to each other takes 0.4-0.6 us of its 0.9), so few wide shares
+  // win over many narrow tiles.
+  const int64_t tiles = (int64_t)((a.T + 127) / 128) * ((a.N + 255) / 256), G = a.K / 64;
+  int shares = 1;
+  while (shares < 8 && tiles * shares * 2 <= sms && G / (2 * shares) >= 4) shares *= 2;
   // without the shrink between them the GEMM follows the layout directly, and waits for it
-  if (rows * ((a.N + 255) / 256) * 4 >= 3 * (int64_t)sms) {
-    err = base<BaseCfg<256, 4>>(a, 1, adapters, s);
-  } else if (rows * ((a.N + 127) / 128) * 2 >= sms) {
-    err = base<BaseCfg<128, 6>>(a, shares(rows * ((a.N + 127) / 128)), adapters, s);
-  } else {
-    err = base<BaseCfg<64, 8>>(a, shares(rows * ((a.N + 63) / 64)), adapters, s);
-  }
+  err = base<BaseCfg<256, 4>>(a, shares, adapters, s);
   if (err != cudaSuccess || a.n == 0) return err;
   return launch_lora_expand(a, a.us, a.B, true, a.N, a.out, s);
 }

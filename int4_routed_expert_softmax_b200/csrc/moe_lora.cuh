@@ -2,6 +2,8 @@
 // moe_lora_bwd.cu): warp-level matrix products and the packed fp32 arithmetic.
 #pragma once
 
+#include <atomic>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -158,6 +160,20 @@ inline cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_
   cfg.attrs = &at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// A kernel that splits its registers with setmaxnreg counts on those it was
+// launched with: a build that gave it others would leave setmaxnreg.inc
+// waiting, and is refused.  `known`: the kernel's own record of its count.
+template <typename K>
+inline cudaError_t launch_regs_ok(K kernel, int want, std::atomic<int> &known) {
+  if (known.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes fa{};
+    const cudaError_t err = cudaFuncGetAttributes(&fa, kernel);
+    if (err != cudaSuccess) return err;
+    known.store(fa.numRegs, std::memory_order_relaxed);
+  }
+  return known.load(std::memory_order_relaxed) == want ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
 // At most this many tiles of kLoraSeg tokens of one adapter (each adapter's

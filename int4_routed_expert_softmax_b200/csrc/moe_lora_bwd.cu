@@ -234,9 +234,9 @@ __global__ void __launch_bounds__(256) k_lora_gsplit(const LoraArgs a) {
 }
 
 // ===========================================================================
-// dx = g W^: tiles of 128 tokens by 256 inputs, one CTA each.  Warp 0 loads
+// dx = g W^: tiles of 128 tokens by 256 inputs, one CTA each.  Warp 8 loads
 // (TMA, two stages of 64 of the N reduction: 128 + 256 rows of hi and lo),
-// warp 1 issues the MMAs, warps 2-9 hold the sums in registers: a warp has one
+// warp 9 issues the MMAs, warps 0-7 hold the sums in registers: a warp has one
 // quarter of the tokens (its TMEM lanes) by half of the inputs.  They add the
 // accumulator every kDxFlush stages, two accumulators taking turns, because
 // the tensor cores truncate (one accumulator over N = 6144 was off by 2.2e-5;
@@ -248,7 +248,12 @@ constexpr int kDxFlush = 2;
 constexpr uint32_t kDxA = kDxTok * 128, kDxB = kDxCol * 128;      // one of hi, lo
 constexpr uint32_t kDxStage = 2 * (kDxA + kDxB);
 constexpr size_t kDxSmem = 1024 + (size_t)kDxStages * kDxStage + 1024;  // barriers, stages, alignment
-constexpr int kDxThreads = 10 * 32;
+// Launched at 168 registers a thread; the two epilogue warpgroups take 216, the
+// third gives its own down to 72: 2 * 128 * 216 + 128 * 72 = 384 * 168.
+constexpr int kDxThreads = 384, kDxLaunchRegs = 168, kDxRegs = 216, kDxRegsOther = 72;
+static_assert(2 * 128 * kDxRegs + 128 * kDxRegsOther <= kDxThreads * kDxLaunchRegs,
+              "register split exceeds the launch's registers");
+constexpr int kDxTmaWarp = 8, kDxMmaWarp = 9;
 
 __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, const __grid_constant__ CUtensorMap gmap,
                                                            const __grid_constant__ CUtensorMap wmap) {
@@ -275,7 +280,7 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
     mbar_init(done, 1);
     fence_barrier_init();
   }
-  if (warp == 1) {
+  if (warp == kDxMmaWarp) {
     tmem_alloc(tmem_slot, 2 * kDxCol);
     tmem_relinquish();
   }
@@ -283,97 +288,113 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDxRegsOther));
+    if (warp == kDxTmaWarp) {
       int issued = 0;
       for (int j = 0; j < S; ++j) {
         const int s = j % kDxStages;
-        if (j >= kDxStages && !mbar_wait(empty + s, (uint32_t)(j / kDxStages - 1) & 1u, a.status, kDetLoraEmpty,
-                                         a.wait_limit)) {
+        if ((j >= kDxStages &&
+             !warp_wait(empty + s, (uint32_t)(j / kDxStages - 1) & 1u, a.status, kDetLoraEmpty, a.wait_limit)) ||
+            __any_sync(0xffffffffu, *abort_flag != 0)) {
           *abort_flag = 1;
           break;
         }
-        unsigned char *b = buf + s * kDxStage;
-        mbar_arrive_expect_tx(full + s, kDxStage);
-        tma_load_2d(b, &gmap, j * 128, t0, full + s);
-        tma_load_2d(b + kDxA, &gmap, j * 128 + 64, t0, full + s);
-        tma_load_2d(b + 2 * kDxA, &wmap, j * 128, k0, full + s);
-        tma_load_2d(b + 2 * kDxA + kDxB, &wmap, j * 128 + 64, k0, full + s);
+        if (elect_one()) {
+          unsigned char *b = buf + s * kDxStage;
+          mbar_arrive_expect_tx(full + s, kDxStage);
+          tma_load_2d(b, &gmap, j * 128, t0, full + s);
+          tma_load_2d(b + kDxA, &gmap, j * 128 + 64, t0, full + s);
+          tma_load_2d(b + 2 * kDxA, &wmap, j * 128, k0, full + s);
+          tma_load_2d(b + 2 * kDxA + kDxB, &wmap, j * 128 + 64, k0, full + s);
+        }
+        __syncwarp();
         issued = j + 1;
-        if (*abort_flag) break;
       }
       for (int j = max(0, issued - kDxStages); j < issued; ++j)
         mbar_drain(full + j % kDxStages, (uint32_t)(j / kDxStages) & 1u, a.status, kDetLoraDrain);
     }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
+    if (warp == kDxMmaWarp) {
       const uint32_t idesc = pf_idesc(kDxCol);
+      const uint64_t ad0 = umma_desc_sw128(smem_u32(buf));
       for (int j = 0; j < S; ++j) {
         const int s = j % kDxStages, c = j / kDxFlush;
         const bool first = j % kDxFlush == 0;
-        if (!mbar_wait(full + s, (uint32_t)(j / kDxStages) & 1u, a.status, kDetLoraFull, a.wait_limit) ||
+        if (!warp_wait(full + s, (uint32_t)(j / kDxStages) & 1u, a.status, kDetLoraFull, a.wait_limit) ||
             (first && c >= 2 &&
-             !mbar_wait(accfree + (c & 1), (uint32_t)(c / 2 - 1) & 1u, a.status, kDetLoraFree, a.wait_limit)) ||
-            *abort_flag) {
+             !warp_wait(accfree + (c & 1), (uint32_t)(c / 2 - 1) & 1u, a.status, kDetLoraFree, a.wait_limit)) ||
+            __any_sync(0xffffffffu, *abort_flag != 0)) {
           *abort_flag = 1;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)((c & 1) * kDxCol);
-        const uint64_t ad = umma_desc_sw128(smem_u32(buf + s * kDxStage));
-        const uint64_t bd = umma_desc_sw128(smem_u32(buf + s * kDxStage + 2 * kDxA));
+        const uint64_t ad = ad0 + (uint64_t)((s * kDxStage) >> 4), bd = ad + (uint64_t)((2 * kDxA) >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t o = (uint64_t)((k * 32) >> 4);
-          umma_f16(d, ad + o, bd + o + (kDxB >> 4), idesc, (uint32_t)(!first || k > 0));
-          umma_f16(d, ad + o + (kDxA >> 4), bd + o, idesc, 1u);
-          umma_f16(d, ad + o, bd + o, idesc, 1u);
+          for (int k = 0; k < 4; ++k) {
+            const uint64_t o = (uint64_t)((k * 32) >> 4);
+            umma_f16(d, ad + o, bd + o + (kDxB >> 4), idesc, (uint32_t)(!first || k > 0));
+            umma_f16(d, ad + o + (kDxA >> 4), bd + o, idesc, 1u);
+            umma_f16(d, ad + o, bd + o, idesc, 1u);
+          }
+          umma_commit(empty + s);
+          if (j % kDxFlush == kDxFlush - 1 || j == S - 1) umma_commit(accfull + (c & 1));
         }
-        umma_commit(empty + s);
-        if (j % kDxFlush == kDxFlush - 1 || j == S - 1) umma_commit(accfull + (c & 1));
+        __syncwarp();
       }
-      umma_commit(done);
+      if (elect_one()) umma_commit(done);
+      __syncwarp();
       mbar_drain(done, 0, a.status, kDetLoraDrain);
     }
     __syncwarp();
   } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;  // TMEM lane quarter, half of the inputs
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDxRegs));
+    const int q = warp & 3, half = warp >> 2;  // TMEM lane quarter, half of the inputs
     const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * (kDxCol / 2));
-    float acc[kDxCol / 2];
+    f32x2 acc[kDxCol / 4];
 #pragma unroll
-    for (int i = 0; i < kDxCol / 2; ++i) acc[i] = 0.0f;
-    bool ok = true;
-    for (int c = 0; c < C && ok; ++c) {
+    for (int i = 0; i < kDxCol / 4; ++i) acc[i] = 0ull;
+    for (int c = 0; c < C; ++c) {
       const bool got = mbar_wait(accfull + (c & 1), (uint32_t)(c / 2) & 1u, a.status, kDetLoraAcc, a.wait_limit);
-      ok = __all_sync(0xffffffffu, got && *abort_flag == 0);
-      if (!ok) break;
+      if (!__all_sync(0xffffffffu, got && *abort_flag == 0)) {
+        *abort_flag = 1;
+        break;
+      }
       tc_fence_after();
+      const uint32_t ta = at + (uint32_t)((c & 1) * kDxCol);
+      // 16 columns at a time, the next ones on their way out of tensor memory meanwhile
+      uint32_t v[2][16];
+      tmem_ld16(ta, v[0]);
 #pragma unroll
       for (int i = 0; i < kDxCol / 2; i += 16) {
-        uint32_t v[16];
-        tmem_ld16(at + (uint32_t)((c & 1) * kDxCol + i), v);
+        const int b = (i >> 4) & 1;
         tmem_ld_wait();
+        if (i + 16 < kDxCol / 2) {
+          tmem_ld16(ta + (uint32_t)(i + 16), v[b ^ 1]);
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(accfree + (c & 1));
+        }
 #pragma unroll
-        for (int x = 0; x < 16; ++x) acc[i + x] += __uint_as_float(v[x]);
+        for (int x = 0; x < 16; x += 2) acc[(i + x) / 2] = add2(acc[(i + x) / 2], pack2i(v[b][x], v[b][x + 1]));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(accfree + (c & 1));
     }
-    if (!ok) *abort_flag = 1;
     const int t = t0 + q * 32 + lane, kc = k0 + half * (kDxCol / 2);
-    if (ok && t < a.T) {
+    if (*abort_flag == 0 && t < a.T) {
       const float f = a.gexp[t];
+      const f32x2 f2 = pack2(f, f);
       float *row = a.dx + (size_t)t * a.K + kc;
 #pragma unroll
       for (int i = 0; i < kDxCol / 2; i += 4)
         if (kc + i < a.K)
-          *reinterpret_cast<float4 *>(row + i) = make_float4(f * acc[i], f * acc[i + 1], f * acc[i + 2], f * acc[i + 3]);
+          *reinterpret_cast<ulonglong2 *>(row + i) = make_ulonglong2(mul2(f2, acc[i / 2]), mul2(f2, acc[i / 2 + 1]));
     }
   }
+  tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kDxMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 2 * kDxCol);
   }
@@ -402,6 +423,8 @@ cudaError_t base_dx(const LoraArgs &a, cudaStream_t s) {
   if (err != cudaSuccess) return err;
   static int smem_set[64] = {0};
   err = ensure_smem(k_lora_dx, kDxSmem, smem_set);
+  static std::atomic<int> regs{0};
+  if (err == cudaSuccess) err = launch_regs_ok(k_lora_dx, kDxLaunchRegs, regs);
   if (err != cudaSuccess) return err;
   k_lora_wexp<<<(unsigned)((a.N + 7) / 8), 256, 0, s>>>(a);
   k_lora_wt<<<dim3((unsigned)(Np / 64), (unsigned)(a.K / 64)), 256, 0, s>>>(a);

@@ -174,12 +174,6 @@ __device__ __forceinline__ void tmap_acquire(const CUtensorMap *m) {
   asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(m) : "memory");
 }
 
-// All lanes of the warp wait on `bar` (bounded); false when it ran out.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status, int32_t det,
-                                          long long limit) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, det, limit));
-}
-
 // D[tmem] (+)= A[tmem] * B[smem]^T, fp16 x fp16 -> fp32, issued by one thread.
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
                                             uint32_t accumulate) {

@@ -31,6 +31,22 @@ __device__ __forceinline__ void fence_proxy_async() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// All lanes of the warp wait on `bar` (bounded); false when it ran out.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, int32_t *status, int32_t det,
+                                          long long limit) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, det, limit));
+}
+
+// One lane of a converged warp.  tcgen05 and TMA instructions take their operands
+// from uniform registers: issued under this predicate in a loop that the whole
+// warp runs, they cost what they should; under `lane == 0` each one was led
+// through the code for a divergent thread (83 clocks per MMA).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T, fp16 x fp16 -> fp32, issued by one thread.
 __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                          uint32_t accumulate) {
