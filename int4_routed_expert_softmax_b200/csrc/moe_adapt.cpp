@@ -64,9 +64,9 @@ LoraLayout lora_layout(const moe_lora_dims &p, int T, bool backward) {
     L.xs = seg((size_t)kLoraSmallT / 2 * (K / 64) * kXs * 4);
     L.upart = seg((K + kLoraSlice - 1) / kLoraSlice * (size_t)kLoraSmallT * r * 4);
     if (T > kLoraSmallT) {
-      L.xh = seg(Tp * K * 2);
+      L.xh = seg(Tp * K * 4);
       L.wh = seg(N * K * 2);
-      L.xd = seg(K / 64 * Tp * 8);
+      L.xd = seg(K / 64 * Tp * 4);
       L.ws = seg(K / 64 * align_up(N, kLoraColTile) * 4);
     }
   }

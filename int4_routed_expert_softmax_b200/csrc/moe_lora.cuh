@@ -53,6 +53,12 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// A value as fp16 hi + lo, 22 significant bits within fp16's range.
+__device__ __forceinline__ void split_f16(float v, __half &hi, __half &lo) {
+  hi = __float2half_rn(v);
+  lo = __float2half_rn(v - __half2float(hi));
+}
+
 // The tensor cores truncate their fp32 sums, so a long chain of MMAs into one
 // accumulator shrinks it by about 2^-24 of its size each time (measured: 1.2e-5
 // after 200).  Sums therefore start at zero for a few MMAs and are added to

@@ -38,11 +38,6 @@ __device__ __forceinline__ float pow2_to_15(float m) {
   return __uint_as_float((uint32_t)(k + 127) << 23);
 }
 
-__device__ __forceinline__ void split_f16(float v, __half &hi, __half &lo) {
-  hi = __float2half_rn(v);
-  lo = __float2half_rn(v - __half2float(hi));
-}
-
 // ===========================================================================
 // dA, dB: D[j][l] = sum over the adapter's tokens of left[p][j] right[t][l].
 // left: fp32 rows of r by position (or by token, `left_by_token`, then times
