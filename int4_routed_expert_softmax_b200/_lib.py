@@ -302,92 +302,108 @@ def moe_lora_workspace_bytes(p: MoeLoraDims, T_max: int, backward: bool = False)
     return int(lib().moe_lora_workspace_bytes(ctypes.byref(p), T_max, 1 if backward else 0))
 
 
-def _lora_args(p: MoeLoraDims, T: int, W, A, B, scale, adapter):
+def _on(t, name: str, cols: int) -> tuple[int, int]:
+    """(rows, device) of t [T][cols] float32, which must be on the current device."""
+    T = _rows(t, name, cols)
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current device ({torch.cuda.current_device()}), is on {dev}")
+    return T, dev
+
+
+def _adr(t, name: str, dtype, numel: int, dev: int):
+    """The address of a tensor that _arg accepts and that lies on device `dev`."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _arg(t, name, dtype, numel)
+    raise ValueError(f"{name} must be on device {dev}, is on {t.get_device()}")
+
+
+def _raw_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _lora_adr(p: MoeLoraDims, T: int, W, A, B, scale, adapter, dev: int):
     N, K, n, r = p.N, p.K, p.n_adapters, p.rank
+    w = _adr(W, "W", torch.uint8, N * K // 2 + N * K // 32, dev)
+    if n == 0:
+        return w, None, None, None, None
     dt = torch.bfloat16 if p.dtype == 1 else torch.float16
-    none = n == 0
-    _arg(W, "W", torch.uint8, N * K // 2 + N * K // 32)
-    _arg(A, "A", dt, n * r * K, optional=none)
-    _arg(B, "B", dt, n * N * r, optional=none)
-    _arg(scale, "scale", torch.float32, n, optional=none)
-    _arg(adapter, "adapter", torch.int32, T, optional=none)
+    return (w, _adr(A, "A", dt, n * r * K, dev), _adr(B, "B", dt, n * N * r, dev),
+            _adr(scale, "scale", torch.float32, n, dev), _adr(adapter, "adapter", torch.int32, T, dev))
 
 
 def moe_lora_forward(p: MoeLoraDims, x, W, A, B, scale, adapter, out, ws, u=None, stream=None):
     """out[t] = W^ Q8_0(x_t) + scale_a B_a (A_a x_t), a = adapter[t] (none outside [0, n_adapters)).
     W: uint8, one int4 gs64 matrix (packed bytes, then scales); A [n][rank][K], B [n][N][rank];
-    u [T][rank] (optional): A_a x_t, for the backward."""
-    T = _rows(x, "x", p.K)
-    _lora_args(p, T, W, A, B, scale, adapter)
-    _arg(out, "out", torch.float32, T * p.N)
-    _arg(u, "u", torch.float32, T * p.rank, optional=True)
-    _arg(ws, "ws", torch.uint8)
+    u [T][rank] (optional): A_a x_t, for the backward.  Every tensor on the current device."""
+    T, dev = _on(x, "x", p.K)
+    f32 = torch.float32
     _check("moe_lora_forward", lib().moe_lora_forward(
-        ctypes.byref(p), T, _ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(scale), _ptr(adapter), _ptr(out), _ptr(u),
-        _ptr(ws), ws.numel(), _stream(stream)))
+        p, T, x.data_ptr(), *_lora_adr(p, T, W, A, B, scale, adapter, dev), _adr(out, "out", f32, T * p.N, dev),
+        None if u is None else _adr(u, "u", f32, T * p.rank, dev), _adr(ws, "ws", torch.uint8, 0, dev), ws.numel(),
+        _raw_stream(stream, dev)))
 
 
 def moe_lora_backward(p: MoeLoraDims, g, x, W, A, B, scale, adapter, ws, u=None, dx=None, dA=None, dB=None,
                       stream=None):
     """Gradients of moe_lora_forward for g [T][N]: dx [T][K], dA [n][rank][K], dB [n][N][rank], all float32,
-    each optional.  u: the forward's A x (computed again without it)."""
-    T = _rows(x, "x", p.K)
-    if _rows(g, "g", p.N) != T:
+    each optional.  u: the forward's A x (computed again without it).  Every tensor on the current device."""
+    T, dev = _on(x, "x", p.K)
+    if _on(g, "g", p.N)[0] != T:
         raise ValueError(f"g has {g.shape[0]} rows, x has {T}")
-    _lora_args(p, T, W, A, B, scale, adapter)
-    _arg(u, "u", torch.float32, T * p.rank, optional=True)
-    _arg(dx, "dx", torch.float32, T * p.K, optional=True)
-    _arg(dA, "dA", torch.float32, p.n_adapters * p.rank * p.K, optional=True)
-    _arg(dB, "dB", torch.float32, p.n_adapters * p.rank * p.N, optional=True)
-    _arg(ws, "ws", torch.uint8)
+    f32, nr = torch.float32, p.n_adapters * p.rank
     _check("moe_lora_backward", lib().moe_lora_backward(
-        ctypes.byref(p), T, _ptr(g), _ptr(x), _ptr(W), _ptr(A), _ptr(B), _ptr(scale), _ptr(adapter), _ptr(u),
-        _ptr(dx), _ptr(dA), _ptr(dB), _ptr(ws), ws.numel(), _stream(stream)))
+        p, T, g.data_ptr(), x.data_ptr(), *_lora_adr(p, T, W, A, B, scale, adapter, dev),
+        None if u is None else _adr(u, "u", f32, T * p.rank, dev),
+        None if dx is None else _adr(dx, "dx", f32, T * p.K, dev),
+        None if dA is None else _adr(dA, "dA", f32, nr * p.K, dev),
+        None if dB is None else _adr(dB, "dB", f32, nr * p.N, dev),
+        _adr(ws, "ws", torch.uint8, 0, dev), ws.numel(), _raw_stream(stream, dev)))
 
 
 def moe_balance_workspace_bytes(d: MoeDims, T_max: int, S_max: int = 1) -> int:
     return int(lib().moe_balance_workspace_bytes(ctypes.byref(d), T_max, S_max))
 
 
-def _balance_args(d: MoeDims, logits, idx, counts, ntok, seg, valid):
-    T = _rows(logits, "logits", d.E)
+def _balance_adr(d: MoeDims, logits, idx, counts, ntok, seg, valid):
+    T, dev = _on(logits, "logits", d.E)
+    i32 = torch.int32
     S = 1
+    sg = None
     if seg is not None:
-        _arg(seg, "seg", torch.int32, 2)
+        sg = _adr(seg, "seg", i32, 2, dev)
         S = seg.numel() - 1
-    _arg(idx, "idx", torch.int32, T * d.k)
-    _arg(valid, "valid", torch.uint8, T, optional=True)
-    _arg(counts, "counts", torch.int32, S * d.E)
-    _arg(ntok, "ntok", torch.int32, S)
-    return T, S
+    return (T, S, dev, sg, logits.data_ptr(), _adr(idx, "idx", i32, T * d.k, dev),
+            None if valid is None else _adr(valid, "valid", torch.uint8, T, dev),
+            _adr(counts, "counts", i32, S * d.E, dev), _adr(ntok, "ntok", i32, S, dev))
 
 
 def moe_balance_forward(d: MoeDims, logits, idx, counts, ntok, pmean, loss, ws, seg=None, valid=None, stream=None):
     """Balance loss per segment of packed tokens: counts [S][E] and ntok [S] int32, pmean [S][E] and
     loss [S] float32 from logits [T][E] and idx [T][k].  seg: [S+1] int32 token offsets (one segment
-    without it); valid: [T] uint8, 0 for tokens that are not counted."""
-    T, S = _balance_args(d, logits, idx, counts, ntok, seg, valid)
-    _arg(pmean, "pmean", torch.float32, S * d.E)
-    _arg(loss, "loss", torch.float32, S)
-    _arg(ws, "ws", torch.uint8)
+    without it); valid: [T] uint8, 0 for tokens that are not counted.  Every tensor on the current device."""
+    T, S, dev, *adr = _balance_adr(d, logits, idx, counts, ntok, seg, valid)
     _check("moe_balance_forward", lib().moe_balance_forward(
-        ctypes.byref(d), T, S, _ptr(seg), _ptr(logits), _ptr(idx), _ptr(valid), _ptr(counts), _ptr(ntok),
-        _ptr(pmean), _ptr(loss), _ptr(ws), ws.numel(), _stream(stream)))
+        d, T, S, *adr, _adr(pmean, "pmean", torch.float32, S * d.E, dev), _adr(loss, "loss", torch.float32, S, dev),
+        _adr(ws, "ws", torch.uint8, 0, dev), ws.numel(), _raw_stream(stream, dev)))
 
 
 def moe_balance_backward(d: MoeDims, logits, idx, counts, ntok, dloss, dlogits, seg=None, valid=None, w=None,
                          dw=None, stream=None):
     """dlogits [T][E] for dloss [S] and, with w and dw [T][k], for the gradient of the kept weights."""
-    T, S = _balance_args(d, logits, idx, counts, ntok, seg, valid)
-    _arg(dloss, "dloss", torch.float32, S)
-    _arg(dlogits, "dlogits", torch.float32, T * d.E)
+    T, S, dev, *adr = _balance_adr(d, logits, idx, counts, ntok, seg, valid)
     if (w is None) != (dw is None):
         raise ValueError("w and dw come together")
-    _arg(w, "w", torch.float32, T * d.k, optional=True)
-    _arg(dw, "dw", torch.float32, T * d.k, optional=True)
+    f32 = torch.float32
     _check("moe_balance_backward", lib().moe_balance_backward(
-        ctypes.byref(d), T, S, _ptr(seg), _ptr(logits), _ptr(idx), _ptr(valid), _ptr(counts), _ptr(ntok),
-        _ptr(dloss), _ptr(w), _ptr(dw), _ptr(dlogits), _stream(stream)))
+        d, T, S, *adr, _adr(dloss, "dloss", f32, S, dev),
+        None if w is None else _adr(w, "w", f32, T * d.k, dev),
+        None if dw is None else _adr(dw, "dw", f32, T * d.k, dev), _adr(dlogits, "dlogits", f32, T * d.E, dev),
+        _raw_stream(stream, dev)))
 
 
 # ----------------------------------------------------------------- helpers

@@ -72,22 +72,38 @@ __device__ __forceinline__ void softmax_row(float (&v)[NI]) {
   for (int i = 0; i < NI; ++i) v[i] *= inv;
 }
 
-// Segment bounds, clamped so that no offset, however wrong, leaves [0, T].
-__device__ __forceinline__ int seg_at(const BalanceArgs &a, int s) {
-  if (a.seg == nullptr) return s == 0 ? 0 : a.T;
-  return min(max(a.seg[s], 0), a.T);
-}
-
-// First segment that ends behind t (S if none): the offsets do not decrease.
-__device__ __forceinline__ int seg_of(const BalanceArgs &a, int t) {
-  if (a.seg == nullptr) return 0;
-  int lo = 0, hi = a.S;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (seg_at(a, mid + 1) > t) hi = mid;
-    else lo = mid + 1;
+// Segment bounds, clamped so that no offset, however wrong, leaves [0, T].  Up
+// to kSegTab of them are copied to shared memory first: a search then waits for
+// global memory once.
+constexpr int kSegTab = 256;
+struct Segments {
+  const int32_t *seg;  // the table in shared memory, or the caller's, or null
+  int S, T;
+  __device__ __forceinline__ int at(int s) const {
+    if (seg == nullptr) return s == 0 ? 0 : T;
+    return min(max(seg[s], 0), T);
   }
-  return lo;
+  // First segment that ends behind t (S if none): the offsets do not decrease.
+  __device__ __forceinline__ int of(int t) const {
+    if (seg == nullptr) return 0;
+    int lo = 0, hi = S;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (at(mid + 1) > t) hi = mid;
+      else lo = mid + 1;
+    }
+    return lo;
+  }
+};
+// Synchronises the CTA.
+__device__ __forceinline__ Segments load_segments(const BalanceArgs &a, int32_t *tab) {
+  Segments sg{a.seg, a.S, a.T};
+  if (a.seg != nullptr && a.S < kSegTab) {
+    for (int i = threadIdx.x; i <= a.S; i += blockDim.x) tab[i] = a.seg[i];
+    sg.seg = tab;
+  }
+  __syncthreads();
+  return sg;
 }
 
 // pmean, counts, ntok and this thread's share of the loss for expert e.
@@ -102,52 +118,76 @@ __device__ __forceinline__ float finish_expert(const BalanceArgs &a, int s, int 
 // they touch, the sums of p, the counts and the counted tokens in slot
 // blockIdx.x + s of the workspace: (CTA, segment) pairs follow each other with
 // both indexes never falling, so their sum is a slot of its own.  A call of one
-// CTA finishes the segments itself.
+// CTA finishes the segments itself.  A warp takes U rows at a time (two of up to
+// 256 experts; more do not fit its registers) while the next U, and what the
+// counts need of them, are on their way: one row at a time ran at 3.4 TB/s.
 template <int NI, int VEC>
 __global__ void __launch_bounds__(kBalThreads) k_balance_fwd(const BalanceArgs a) {
   extern __shared__ float bsm[];
+  constexpr int U = NI <= 8 ? 2 : 1;
   const int E = a.E;
   float *sp = bsm;                                     // [kBalWarps][E] sums of p per warp
   int *sc = reinterpret_cast<int *>(sp + kBalWarps * E);  // [E] counts
+  __shared__ int32_t tab[kSegTab];
   __shared__ int sn[2];                                // counted tokens, two segments in turn
   __shared__ float sl[kBalWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool alone = gridDim.x == 1;
+  pdl_launch_dependents();
   const int t0 = min((int)((int64_t)blockIdx.x * a.chunk), a.T), t1 = min(t0 + a.chunk, a.T);
-  const int s0 = alone ? 0 : seg_of(a, t0);
   if (blockIdx.x == 0 && !alone)
     for (int s = tid; s < a.S; s += kBalThreads) a.ticket[s] = 0u;
   for (int e = tid; e < E; e += kBalThreads) sc[e] = 0;
   if (tid < 2) sn[tid] = 0;
-  __syncthreads();
+  const Segments sg = load_segments(a, tab);
+  const int s0 = alone ? 0 : sg.of(t0);
   int par = 0;
   for (int s = s0; s < a.S; ++s) {
-    const int b0 = max(seg_at(a, s), t0), b1 = min(seg_at(a, s + 1), t1);
+    const int b0 = max(sg.at(s), t0), b1 = min(sg.at(s + 1), t1);
     if (!alone) {
-      if (seg_at(a, s) >= t1) break;
+      if (sg.at(s) >= t1) break;
       if (b0 >= b1) continue;  // empty, or none of its tokens here: its slot is never read
     }
     float acc[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) acc[i] = 0.0f;
     int n = 0;
-    float nx[NI];
-    int t = b0 + warp;
-    if (t < b1) load_row<NI, VEC>(a.logits + (size_t)t * E, E, lane, nx);
-    for (; t < b1; t += kBalWarps) {
-      float v[NI];
+    float nx[U][NI];
+    int ne[U];   // this lane's expert of each row, -1: none
+    bool nv[U];  // the row counts
+    auto load = [&](int t) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) v[i] = nx[i];
-      if (t + kBalWarps < b1) load_row<NI, VEC>(a.logits + (size_t)(t + kBalWarps) * E, E, lane, nx);
-      if (a.valid != nullptr && a.valid[t] == 0) continue;
-      if (lane < a.k) {
-        const int e = a.idx[(size_t)t * a.k + lane];
-        if (e >= 0 && e < E) atomicAdd(sc + e, 1);
+      for (int u = 0; u < U; ++u) {
+        const int tu = t + u * kBalWarps;
+        nv[u] = tu < b1 && (a.valid == nullptr || a.valid[tu] != 0);
+        ne[u] = tu < b1 && lane < a.k ? a.idx[(size_t)tu * a.k + lane] : -1;
+        if (tu < b1) load_row<NI, VEC>(a.logits + (size_t)tu * E, E, lane, nx[u]);
       }
-      softmax_row<NI>(v);
+    };
+    int t = b0 + warp;
+    load(t);
+    while (t < b1) {
+      float v[U][NI];
+      int e[U];
+      bool ok[U];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) acc[i] += v[i];
-      ++n;
+      for (int u = 0; u < U; ++u) {
+        e[u] = ne[u];
+        ok[u] = nv[u];
+#pragma unroll
+        for (int i = 0; i < NI; ++i) v[u][i] = nx[u][i];
+      }
+      t += U * kBalWarps;
+      if (t < b1) load(t);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (!ok[u]) continue;
+        if (e[u] >= 0 && e[u] < E) atomicAdd(sc + e[u], 1);
+        softmax_row<NI>(v[u]);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) acc[i] += v[u][i];
+        ++n;
+      }
     }
     if (lane == 0 && n) atomicAdd(sn + par, n);
 #pragma unroll
@@ -192,27 +232,39 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_fwd(const BalanceArgs a
 }
 
 // Joins the CTAs' sums: block (x, s) takes 32 experts of segment s, lane =
-// expert, the warps take every 16th slot; sums in 64 bits, always in the same
-// order.  The last block of a segment adds the blocks' shares of the loss.
-__global__ void __launch_bounds__(512) k_balance_join(const BalanceArgs a) {
-  __shared__ double rp[16][32];
-  __shared__ int rc[16][32], rn[16];
-  __shared__ bool last;
+// expert, the warps every 32nd slot, five of them at once; sums in 64 bits,
+// always in the same order.  The last block of a segment adds the blocks'
+// shares of the loss.
+__global__ void __launch_bounds__(1024) k_balance_join(const BalanceArgs a) {
+  __shared__ double rp[32][32];
+  __shared__ int rc[32][32], rn[32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int s = blockIdx.y, e = blockIdx.x * 32 + lane;
+  const Segments sg{a.seg, a.S, a.T};
+  const int b0 = sg.at(s), b1 = sg.at(s + 1);
   pdl_wait();
-  const int b0 = seg_at(a, s), b1 = seg_at(a, s + 1);
   double p = 0.0;
   int c = 0, n = 0;
   if (b0 < b1) {
     const int c1 = (b1 - 1) / a.chunk;
-    for (int q = b0 / a.chunk + warp; q <= c1; q += 16) {
-      const size_t slot = (size_t)(q + s);
-      if (e < a.E) {
-        p += (double)a.part_p[slot * a.E + e];
-        c += a.part_c[slot * a.E + e];
+    for (int q0 = b0 / a.chunk + warp; q0 <= c1; q0 += 5 * 32) {
+      float pv[5];
+      int cv[5], nv[5];
+#pragma unroll
+      for (int u = 0; u < 5; ++u) {
+        const int q = q0 + 32 * u;
+        const size_t slot = (size_t)(q + s);
+        const bool in = q <= c1;
+        pv[u] = in && e < a.E ? a.part_p[slot * a.E + e] : 0.0f;
+        cv[u] = in && e < a.E ? a.part_c[slot * a.E + e] : 0;
+        nv[u] = in ? a.part_n[slot] : 0;
       }
-      n += a.part_n[slot];
+#pragma unroll
+      for (int u = 0; u < 5; ++u) {
+        p += (double)pv[u];
+        c += cv[u];
+        n += nv[u];
+      }
     }
   }
   rp[warp][lane] = p;
@@ -221,7 +273,8 @@ __global__ void __launch_bounds__(512) k_balance_join(const BalanceArgs a) {
   __syncthreads();
   if (warp != 0) return;
   p = 0.0, c = 0, n = 0;
-  for (int w = 0; w < 16; ++w) {
+#pragma unroll
+  for (int w = 0; w < 32; ++w) {
     p += rp[w][lane];
     c += rc[w][lane];
     n += rn[w];
@@ -233,8 +286,7 @@ __global__ void __launch_bounds__(512) k_balance_join(const BalanceArgs a) {
     if (blockIdx.x == 0) a.ntok[s] = n;
     a.part_l[(size_t)s * gridDim.x + blockIdx.x] = l;
     __threadfence();
-    last = atomicAdd(a.ticket + s, 1u) == gridDim.x - 1;
-    if (last) {
+    if (atomicAdd(a.ticket + s, 1u) == gridDim.x - 1) {
       __threadfence();
       float sum = 0.0f;
       for (unsigned i = 0; i < gridDim.x; ++i) sum += __ldcg(a.part_l + (size_t)s * gridDim.x + i);
@@ -251,10 +303,11 @@ __global__ void __launch_bounds__(256) k_balance_bwd(const BalanceArgs a) {
   extern __shared__ float bsm[];
   const int E = a.E;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ int32_t tab[kSegTab];
   float *kept = bsm + (size_t)warp * ((E + 3) & ~3);
   if (a.dw != nullptr)
     for (int e = lane; e < E; e += 32) kept[e] = 0.0f;
-  __syncwarp();
+  const Segments sg = load_segments(a, tab);
   const int64_t w = (int64_t)blockIdx.x * 8 + warp;
   const int t0 = (int)min((int64_t)a.T, w * a.chunk), t1 = min(t0 + a.chunk, a.T);
   if (t0 >= t1) return;
@@ -262,17 +315,33 @@ __global__ void __launch_bounds__(256) k_balance_bwd(const BalanceArgs a) {
   float f[NI], cs = 0.0f;
 #pragma unroll
   for (int i = 0; i < NI; ++i) f[i] = 0.0f;
-  float nx[NI];
-  load_row<NI, VEC>(a.logits + (size_t)t0 * E, E, lane, nx);
+  // the next row and its pairs are on their way while a row is worked on
+  float nx[NI], nw = 0.0f, nd = 0.0f;
+  int ne = -1;
+  bool nv = true;
+  auto load = [&](int t) {
+    load_row<NI, VEC>(a.logits + (size_t)t * E, E, lane, nx);
+    if (a.valid != nullptr) nv = a.valid[t] != 0;
+    if (a.dw != nullptr && lane < a.k) {
+      const size_t at = (size_t)t * a.k + lane;
+      ne = a.idx[at];
+      nw = a.w[at];
+      nd = a.dw[at];
+    }
+  };
+  load(t0);
   for (int t = t0; t < t1; ++t) {
     float v[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) v[i] = nx[i];
-    if (t + 1 < t1) load_row<NI, VEC>(a.logits + (size_t)(t + 1) * E, E, lane, nx);
+    const int e = ne;
+    const float wi = nw, di = nd;
+    const bool valid = nv;
+    if (t + 1 < t1) load(t + 1);
     if (t >= s_end) {
-      s = seg_of(a, t);
-      s_begin = s < a.S ? seg_at(a, s) : a.T;
-      s_end = s < a.S ? seg_at(a, s + 1) : a.T;
+      s = sg.of(t);
+      s_begin = s < a.S ? sg.at(s) : a.T;
+      s_end = s < a.S ? sg.at(s + 1) : a.T;
       const int n = s < a.S ? a.ntok[s] : 0;
       cs = n > 0 ? __fdiv_rn(a.dloss[s], (float)n) : 0.0f;
       const float fs = n > 0 ? (float)((double)E / ((double)a.k * n)) : 0.0f;
@@ -282,7 +351,7 @@ __global__ void __launch_bounds__(256) k_balance_bwd(const BalanceArgs a) {
         f[i] = n > 0 && e < E ? (float)a.counts[(size_t)s * E + e] * fs : 0.0f;
       }
     }
-    const bool counted = t >= s_begin && s < a.S && (a.valid == nullptr || a.valid[t] != 0);
+    const bool counted = t >= s_begin && s < a.S && valid;
     if (counted) {
       softmax_row<NI>(v);
       float dot = 0.0f;
@@ -297,14 +366,6 @@ __global__ void __launch_bounds__(256) k_balance_bwd(const BalanceArgs a) {
       for (int i = 0; i < NI; ++i) v[i] = 0.0f;
     }
     if (a.dw != nullptr) {
-      int e = -1;
-      float wi = 0.0f, di = 0.0f;
-      if (lane < a.k) {
-        const size_t at = (size_t)t * a.k + lane;
-        e = a.idx[at];
-        wi = a.w[at];
-        di = a.dw[at];
-      }
       float wd = wi * di;
 #pragma unroll
       for (int off = 16; off >= 1; off >>= 1) wd += __shfl_xor_sync(0xffffffffu, wd, off);
@@ -409,7 +470,7 @@ cudaError_t launch_balance_fwd(const BalanceArgs &a, int grid, cudaStream_t s) {
   if (err != cudaSuccess || grid == 1) return err;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((a.E + 31) / 32), (unsigned)a.S);
-  cfg.blockDim = dim3(512);
+  cfg.blockDim = dim3(1024);
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -70,6 +70,7 @@ enum Detail : int32_t {
   kDetLoraGemmFull = 55,
   kDetLoraGemmEmpty = 56,
   kDetLoraGemmDrain = 57,
+  kDetLoraProj = 58,
 };
 
 // The wait limit kernels launched now take for their work waits (set by
@@ -323,7 +324,7 @@ cudaError_t launch_balance_fwd(const BalanceArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_balance_bwd(const BalanceArgs &a, int sms, cudaStream_t s);
 
 // int4 projection with low-rank adapters (moe_lora.cu, moe_lora_bwd.cu).
-constexpr int kLoraSmallT = 32;      // the largest batch the token-order kernels take
+constexpr int kLoraSmallT = 16;      // the largest batch the small kernels take (their CTAs hold all its codes)
 constexpr int kLoraSlice = 512;      // inputs per CTA of their first kernel
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = 4096;

@@ -82,28 +82,44 @@ __global__ void __launch_bounds__(128) k_lora_in(const LoraArgs a) {
   if (id == a.n) return;
   *reinterpret_cast<float4 *>(xsm + 4 * tid) = v;
   __syncthreads();
-  // rows j = warp, warp + 4, ..: lane = 16 of the slice's inputs (8 + 8)
+  // rows j = warp, warp + 4, .., four of them loaded at once: lane = 16 of the
+  // slice's inputs (8 + 8)
   const uint16_t *A = static_cast<const uint16_t *>(a.A) + (size_t)id * r * a.K + k0;
   float *dst = a.upart + ((size_t)blockIdx.x * a.T + t) * r;
-  for (int j = warp; j < r; j += 4) {
-    float s = 0.0f;
+  for (int j0 = warp; j0 < r; j0 += 16) {
+    uint4 w[4][2];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int i = h * 256 + lane * 8, j = j0 + 4 * m;
+        w[m][h] = j < r && k0 + i < a.K ? __ldg(reinterpret_cast<const uint4 *>(A + (size_t)j * a.K + i))
+                                        : make_uint4(0u, 0u, 0u, 0u);
+      }
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int i = h * 256 + lane * 8;
-      if (k0 + i < a.K) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(A + (size_t)j * a.K + i));
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      const float4 *xp = reinterpret_cast<const float4 *>(xsm + h * 256 + lane * 8);
+      const float4 x0 = xp[0], x1 = xp[1];
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
-          const float2 f = half2_values<BF16>(ww[m]);
-          s = ffma(f.x, xsm[i + 2 * m], s);
-          s = ffma(f.y, xsm[i + 2 * m + 1], s);
-        }
+      for (int m = 0; m < 4; ++m) {
+        const float2 a0 = half2_values<BF16>(w[m][h].x), a1 = half2_values<BF16>(w[m][h].y);
+        const float2 a2 = half2_values<BF16>(w[m][h].z), a3 = half2_values<BF16>(w[m][h].w);
+        s[m] = ffma(a0.x, x0.x, s[m]);
+        s[m] = ffma(a0.y, x0.y, s[m]);
+        s[m] = ffma(a1.x, x0.z, s[m]);
+        s[m] = ffma(a1.y, x0.w, s[m]);
+        s[m] = ffma(a2.x, x1.x, s[m]);
+        s[m] = ffma(a2.y, x1.y, s[m]);
+        s[m] = ffma(a3.x, x1.z, s[m]);
+        s[m] = ffma(a3.y, x1.w, s[m]);
       }
     }
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if (lane == 0) dst[j] = s;
+    for (int off = 16; off >= 1; off >>= 1)
+#pragma unroll
+      for (int m = 0; m < 4; ++m) s[m] += __shfl_xor_sync(0xffffffffu, s[m], off);
+    if (lane < 4 && j0 + 4 * lane < r) dst[j0 + 4 * lane] = lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3];
   }
 }
 
@@ -134,21 +150,48 @@ __device__ __forceinline__ void group_mma(f32x2 (&acc)[2], const NibblePair &w, 
   acc[1] = fma2(th, s1, acc[1]);
 }
 
+// Shared memory of k_lora_proj: the codes and the scales of all tokens as rows
+// padded by 32 bytes, so that the rows that half a warp reads start on
+// different banks; the row sums of the eight warps; scale A x; W's scales.
+struct ProjLayout {
+  int crow, xrow;  // bytes of a row of codes, of a token pair's scales
+  int xs, red, us, ws, total;
+};
+__host__ __device__ inline ProjLayout proj_layout(int K, int r, int NT) {
+  ProjLayout L;
+  L.crow = K + (160 - K % 128) % 128;  // = 32 mod 128
+  L.xrow = K / 64 * kXs * 4 + (160 - K / 64 * kXs * 4 % 128) % 128;
+  L.xs = 16 + NT * 8 * L.crow;
+  L.red = L.xs + NT * 4 * L.xrow;
+  L.us = L.red + 8 * 16 * NT * 8 * 4;
+  L.ws = L.us + NT * 8 * r * 4;
+  L.total = L.ws + 16 * (K / 64) * 2;
+  return L;
+}
+
 template <int NT, bool BF16>
 __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
-  extern __shared__ __align__(16) float psm[];
+  extern __shared__ __align__(128) unsigned char psm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, q4 = lane & 3;
   const int G = a.K / 64, N = a.N, r = a.r, T = a.T;
-  const int Gp = G + 2;
-  float *red = psm;                                            // [8][16][NT * 8]
-  float *us = red + 8 * 16 * NT * 8;                           // [NT * 8][r]
-  __half *ssc = reinterpret_cast<__half *>(us + NT * 8 * r);   // [16][Gp]
+  const ProjLayout L = proj_layout(a.K, r, NT);
+  uint64_t *landed = reinterpret_cast<uint64_t *>(psm);        // the codes and every scale
+  float *red = reinterpret_cast<float *>(psm + L.red);         // [8][16][NT * 8]
+  float *us = reinterpret_cast<float *>(psm + L.us);           // [NT * 8][r]
+  const __half *ssc = reinterpret_cast<const __half *>(psm + L.ws);  // [16][G]
   const int n0 = blockIdx.x * 16;
   const int rl = min(n0 + gq, N - 1), rh = min(n0 + gq + 8, N - 1);  // N may end inside the tile
   const unsigned char *Wl = a.W + (size_t)rl * (a.K / 2) + q4 * 8;
   const unsigned char *Wh = a.W + (size_t)rh * (a.K / 2) + q4 * 8;
-  const __half *sc = reinterpret_cast<const __half *>(a.W + (size_t)N * (a.K / 2));
+  if (tid == 0) {
+    mbar_init(landed, 2);
+    fence_barrier_init();
+    // W's scales do not wait for the kernel before
+    const uint32_t bytes = (uint32_t)(min(16, N - n0) * G * 2);  // N % 8 == 0: a multiple of 16
+    mbar_arrive_expect_tx(landed, bytes);
+    bulk_g2s(psm + L.ws, a.W + (size_t)N * (a.K / 2) + (size_t)n0 * G * 2, bytes, landed);
+  }
   uint2 wl[kProjPre], wh[kProjPre];
   auto load_w = [&](int i0) {
 #pragma unroll
@@ -161,12 +204,34 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
     }
   };
   load_w(0);
-  for (int i = tid; i < 16 * G; i += 256) {
-    const int row = i / G, g = i - row * G;
-    ssc[row * Gp + g] = sc[(size_t)min(n0 + row, N - 1) * G + g];
-  }
+  // this thread's output (the first of them) and its row of B, brought near
+  const int row = tid & 15, t1 = tid >> 4;
+  const int id1 = t1 < T ? adapter_of(a, t1) : a.n;
+  const uint16_t *Bn = static_cast<const uint16_t *>(a.B);
+  if (id1 < a.n && n0 + row < N)
+    asm volatile("prefetch.global.L1 [%0];" ::"l"(Bn + ((size_t)id1 * N + n0 + row) * r) : "memory");
   pdl_wait();
-  __syncthreads();
+  if (tid == 0) {
+    const int pairs = (T + 1) / 2;
+    mbar_arrive_expect_tx(landed, (uint32_t)(T * a.K + pairs * G * kXs * 4));
+    for (int t = 0; t < T; ++t) bulk_g2s(psm + 16 + t * L.crow, a.xq + (size_t)t * a.K, (uint32_t)a.K, landed);
+    for (int i = 0; i < pairs; ++i)
+      bulk_g2s(psm + L.xs + i * L.xrow, a.xs + (size_t)i * G * kXs, (uint32_t)(G * kXs * 4), landed);
+  }
+  // A x of the tokens, the slices in order
+  const int slices = (a.K + kLoraSlice - 1) / kLoraSlice;
+  for (int i = tid; i < T * r; i += 256) {
+    const int t = i / r, id = adapter_of(a, t);
+    float u = 0.0f;
+    if (id < a.n) {
+#pragma unroll 4
+      for (int s = 0; s < slices; ++s) u += a.upart[(size_t)s * T * r + i];
+    }
+    if (blockIdx.x == 0 && a.u != nullptr) a.u[i] = u;
+    us[i] = id < a.n ? a.scale[id] * u : 0.0f;
+  }
+  __syncthreads();  // the barrier is initialised for every thread
+  bool ok = mbar_wait(landed, 0, a.status, kDetLoraProj, a.wait_limit);
   f32x2 acc[NT][2];
 #pragma unroll
   for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = 0ull;
@@ -176,14 +241,14 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
     for (int i = 0; i < kProjPre; ++i) {
       const int g = warp + 8 * (i0 + i);
       if (g < G) {
-        const float s0 = __half2float(ssc[gq * Gp + g]), s1 = __half2float(ssc[(gq + 8) * Gp + g]);
+        const float s0 = __half2float(ssc[gq * G + g]), s1 = __half2float(ssc[(gq + 8) * G + g]);
         const f32x2 p0 = pack2(s0, s0), p1 = pack2(s1, s1);
         const NibblePair w = nibbles(wl[i], wh[i]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const int8_t *cq = a.xq + (size_t)(j * 8 + gq) * a.K + (size_t)g * 64 + q4 * 8;
+          const unsigned char *cq = psm + 16 + (j * 8 + gq) * L.crow + g * 64 + q4 * 8;
           const uint2 b0 = *reinterpret_cast<const uint2 *>(cq), b1 = *reinterpret_cast<const uint2 *>(cq + 32);
-          const float4 *x4 = reinterpret_cast<const float4 *>(a.xs + ((size_t)(j * 4 + q4) * G + g) * kXs);
+          const float4 *x4 = reinterpret_cast<const float4 *>(psm + L.xs + (j * 4 + q4) * L.xrow + g * kXs * 4);
           group_mma(acc[j], w, b0, b1, x4[0], x4[1], p0, p1);
         }
       }
@@ -195,28 +260,23 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
     *reinterpret_cast<float2 *>(o) = unpack2(acc[j][0]);
     *reinterpret_cast<float2 *>(o + 8 * NT * 8) = unpack2(acc[j][1]);
   }
-  // A x of the tokens, the slices in order
-  const int slices = (a.K + kLoraSlice - 1) / kLoraSlice;
-  for (int i = tid; i < T * r; i += 256) {
-    const int t = i / r, id = adapter_of(a, t);
-    float u = 0.0f;
-    if (id < a.n)
-      for (int s = 0; s < slices; ++s) u += a.upart[(size_t)s * T * r + i];
-    if (blockIdx.x == 0 && a.u != nullptr) a.u[i] = u;
-    us[i] = id < a.n ? a.scale[id] * u : 0.0f;
+  if (__syncthreads_or(!ok)) {
+    // a copy may still be on its way: it lands before the CTA ends
+    if (tid == 0) mbar_drain(landed, 0, a.status, kDetLoraProj);
+    return;
   }
-  __syncthreads();
   for (int i = tid; i < 16 * T; i += 256) {
-    const int row = i & 15, t = i >> 4;
+    const int t = i >> 4;  // row stays tid & 15
     if (n0 + row >= N) continue;
     float o = 0.0f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) o += red[(w * 16 + row) * (NT * 8) + t];
     const int id = adapter_of(a, t);
     if (id < a.n) {
-      const uint4 *B = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.B) + ((size_t)id * N + n0 + row) * r);
+      const uint4 *B = reinterpret_cast<const uint4 *>(Bn + ((size_t)id * N + n0 + row) * r);
       const float *ut = us + t * r;
       float l = 0.0f;
+#pragma unroll 2
       for (int j = 0; j < r / 8; ++j) {
         const uint4 w = __ldg(B + j);
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
@@ -919,7 +979,7 @@ cudaError_t shrink_rank(const LoraArgs &a, const float *src, int L, const void *
 
 template <int NT, bool BF16>
 cudaError_t proj(const LoraArgs &a, cudaStream_t s) {
-  const size_t smem = (size_t)(8 * 16 * NT * 8 + NT * 8 * a.r) * 4 + (size_t)16 * (a.K / 64 + 2) * 2;
+  const size_t smem = (size_t)proj_layout(a.K, a.r, NT).total;
   static int smem_set[64] = {0};
   cudaError_t err = ensure_smem(k_lora_proj<NT, BF16>, smem, smem_set);
   if (err != cudaSuccess) return err;
@@ -932,8 +992,7 @@ cudaError_t small(const LoraArgs &a, cudaStream_t s) {
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess) return err;
   if (a.T <= 8) return proj<1, BF16>(a, s);
-  if (a.T <= 16) return proj<2, BF16>(a, s);
-  return proj<4, BF16>(a, s);
+  return proj<2, BF16>(a, s);
 }
 
 // How many clusters of `shares` CTAs of k_lora_base fit on the device at once
