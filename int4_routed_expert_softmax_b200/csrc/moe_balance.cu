@@ -10,66 +10,140 @@
 //   kept part: for slot i, w_i (dw_i - sum_j w_j dw_j) at e = idx[t][i]
 //   (w = softmax over the kept logits).
 //
-// Both directions read each logit once and are bound by that traffic: a warp
-// holds one row in registers (lane = a few experts), two shuffle trees give
-// its maximum and its sum, and the next row's loads are in flight meanwhile.
-// The backward recomputes p, which costs less than reading T * E saved values.
-#include <cfloat>
-
-#include "moe_device.cuh"
+// Both directions read each logit once and are bound by that traffic, with the
+// instructions per row close behind: a row therefore goes to L lanes of a warp
+// (8 up to 256 experts), which hold NV values each, and a warp works on 32 / L
+// rows at once, so that the shuffle trees, the loop and the addresses serve four
+// rows (one row per warp: 186 instructions a row forward, 34 us for 131072 by
+// 256; 329 and 83 us backward).  Rows come through a ring of asynchronous copies
+// per warp.  The backward recomputes p, which costs less than reading T * E
+// saved values.
+#include "moe_lora.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kBalThreads = 512;
-constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kFwdThreads = 256, kFwdWarps = kFwdThreads / 32;
+constexpr int kBwdThreads = 256, kBwdWarps = kBwdThreads / 32;
 
-// Expert of a lane's i-th value.  VEC = 4: 16-byte loads (E % 4 == 0 and a
-// 16-byte aligned base); VEC = 1: any E.
-template <int VEC>
-__device__ __forceinline__ int expert_of(int i, int lane) {
-  return VEC == 4 ? (i >> 2) * 128 + lane * 4 + (i & 3) : i * 32 + lane;
+// Expert of a lane's i-th value; `sub`: the lane's place among its row's L.
+// VEC = 4: 16-byte accesses (E % 4 == 0 and 16-byte aligned rows); VEC = 1: any E.
+template <int L, int VEC>
+__device__ __forceinline__ int expert_of(int i, int sub) {
+  return VEC == 4 ? (i >> 2) * (4 * L) + sub * 4 + (i & 3) : i * L + sub;
 }
 
-template <int NI, int VEC>
-__device__ __forceinline__ void load_row(const float *row, int E, int lane, float (&v)[NI]) {
-  if (VEC == 4) {
-#pragma unroll
-    for (int j = 0; j < NI / 4; ++j) {
-      const int e = j * 128 + lane * 4;
-      const float4 q = e < E ? __ldcs(reinterpret_cast<const float4 *>(row + e))
-                             : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int e = i * 32 + lane;
-      v[i] = e < E ? __ldcs(row + e) : -INFINITY;
-    }
+// A warp's own ring in shared memory: R turns of 32 / L rows, each row copied
+// there asynchronously R turns before its own (16 bytes a lane, or 4 where E or
+// the address allow no more), with the row's k experts behind it and, if W2, its
+// kept weights and their gradients.  Nothing is shared between warps, so there
+// is nothing to wait for but the warp's own copies.  Rows of kWords words (8
+// more than a multiple of 32: four rows' 4-byte reads then use all banks).
+template <int L, int NV, int VEC, bool W2>
+struct RowRing {
+  static constexpr int R = NV <= 8 ? 4 : NV == 16 ? 3 : 2;  // turns of 32 NV words: two CTAs per SM hold theirs
+  static constexpr int kCols = L * NV, kWords = kCols + (W2 ? 96 : 32) + 8, kRows = 32 / L;
+  static constexpr int kTotal = R * kRows * kWords;
+  float *mine;  // this lane's row of slot 0
+  const BalanceArgs &a;
+  int sub;
+  __device__ __forceinline__ RowRing(float *mem, const BalanceArgs &args, int lane)
+      : mem_(mem), a(args), sub(lane % L) {
+    mine = mem + (lane / L) * kWords;
   }
+  float *mem_;
+  __device__ __forceinline__ static void copy4(float *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+  }
+  __device__ __forceinline__ void issue(int slot, int t, bool in) const {
+    float *dst = mine + slot * (kRows * kWords);
+    if (in) {
+      const float *row = a.logits + (size_t)t * a.E;
+#pragma unroll
+      for (int i = 0; i < NV; i += VEC) {
+        const int e = expert_of<L, VEC>(i, sub);
+        if (e < a.E) {
+          if (VEC == 4) cp_async16(dst + e, row + e);
+          else copy4(dst + e, row + e);
+        }
+      }
+      if (a.idx != nullptr)
+        for (int j = sub; j < a.k; j += L) {
+          const size_t at = (size_t)t * a.k + j;
+          copy4(dst + kCols + j, a.idx + at);
+          if (W2) {
+            copy4(dst + kCols + 32 + j, a.w + at);
+            copy4(dst + kCols + 64 + j, a.dw + at);
+          }
+        }
+    }
+    cp_async_commit();
+  }
+  // This lane's values of its row of a slot (-inf beyond E), once all but the
+  // newest R - 1 turns have landed; returns what lies behind the row.
+  __device__ __forceinline__ float *take(int slot, f32x2 (&v)[NV / 2]) const {
+    cp_async_wait<R - 1>();
+    __syncwarp();
+    float *src = mine + slot * (kRows * kWords);
+#pragma unroll
+    for (int i = 0; i < NV; i += VEC == 4 ? 4 : 2) {
+      const int e = expert_of<L, VEC>(i, sub);
+      const f32x2 none = pack2(-INFINITY, -INFINITY);
+      if (VEC == 4) {
+        const ulonglong2 q = e < a.E ? *reinterpret_cast<const ulonglong2 *>(src + e) : make_ulonglong2(none, none);
+        v[i / 2] = q.x, v[i / 2 + 1] = q.y;
+      } else {
+        v[i / 2] = pack2(e < a.E ? src[e] : -INFINITY, e + L < a.E ? src[e + L] : -INFINITY);
+      }
+    }
+    return src + kCols;
+  }
+};
+
+// Sum and maximum over a row's L lanes.
+template <int L>
+__device__ __forceinline__ float row_add(float v) {
+#pragma unroll
+  for (int off = L / 2; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int off = L / 2; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
-// v -> softmax of the row (a row of -inf alone, which leaves no expert, gives
-// 0 everywhere; NaN and +inf give NaN).
-template <int NI>
-__device__ __forceinline__ void softmax_row(float (&v)[NI]) {
-  float m = v[0];
+// v -> exp(v - m) in place, and in `inv` what makes them probabilities: e^x =
+// 2^(x log2 e), whose exponent is off by 2^-23 of itself at most, so 2^-23 |x| of
+// the value.  A row of -inf alone, which leaves no expert, gives 0 everywhere;
+// NaN and +inf give NaN.
+template <int L, int NV>
+__device__ __forceinline__ void softmax_row(f32x2 (&v)[NV / 2], float &inv) {
+  float m = -INFINITY;
 #pragma unroll
-  for (int i = 1; i < NI; ++i) m = fmaxf(m, v[i]);
-  m = warp_max(m);
+  for (int i = 0; i < NV / 2; ++i) {
+    const float2 x = unpack2(v[i]);
+    m = fmaxf(fmaxf(m, x.x), x.y);
+  }
+  m = row_max<L>(m);
   if (m == -INFINITY) m = 0.0f;  // every term is then exp(-inf) = 0 (or NaN for a NaN)
-  float s = 0.0f;
+  const f32x2 m2 = pack2(-m, -m), l2 = pack2(1.44269504f, 1.44269504f);
+  f32x2 s = 0ull;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    v[i] = expf(v[i] - m);
-    s += v[i];
+  for (int i = 0; i < NV / 2; ++i) {
+    const float2 x = unpack2(mul2(add2(v[i], m2), l2));
+    v[i] = pack2(exp2_fast(x.x), exp2_fast(x.y));
+    s = add2(s, v[i]);
   }
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-  const float inv = s == 0.0f ? 0.0f : __fdiv_rn(1.0f, s);
-#pragma unroll
-  for (int i = 0; i < NI; ++i) v[i] *= inv;
+  const float2 h = unpack2(s);
+  const float sum = row_add<L>(h.x + h.y);
+  inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
 }
 
 // Segment bounds, clamped so that no offset, however wrong, leaves [0, T].  Up
@@ -118,26 +192,26 @@ __device__ __forceinline__ float finish_expert(const BalanceArgs &a, int s, int 
 // they touch, the sums of p, the counts and the counted tokens in slot
 // blockIdx.x + s of the workspace: (CTA, segment) pairs follow each other with
 // both indexes never falling, so their sum is a slot of its own.  A call of one
-// CTA finishes the segments itself.  A warp takes U rows at a time (two of up to
-// 256 experts; more do not fit its registers) while the next U, and what the
-// counts need of them, are on their way: one row at a time ran at 3.4 TB/s.
-template <int NI, int VEC>
-__global__ void __launch_bounds__(kBalThreads) k_balance_fwd(const BalanceArgs a) {
-  extern __shared__ float bsm[];
-  constexpr int U = NI <= 8 ? 2 : 1;
+// CTA finishes the segments itself.
+template <int L, int NV, int VEC>
+__global__ void __launch_bounds__(kFwdThreads) k_balance_fwd(const BalanceArgs a) {
+  extern __shared__ __align__(16) float bsm[];
+  using Ring = RowRing<L, NV, VEC, false>;
+  constexpr int R = Ring::R, kRows = Ring::kRows, kTurn = kFwdWarps * kRows;  // rows of the CTA per turn
   const int E = a.E;
-  float *sp = bsm;                                     // [kBalWarps][E] sums of p per warp
-  int *sc = reinterpret_cast<int *>(sp + kBalWarps * E);  // [E] counts
+  float *sp = bsm;                                          // [kFwdWarps][E] sums of p per warp
+  int *sc = reinterpret_cast<int *>(sp + kFwdWarps * E);    // [E] counts
   __shared__ int32_t tab[kSegTab];
-  __shared__ int sn[2];                                // counted tokens, two segments in turn
-  __shared__ float sl[kBalWarps];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ int sn[2];                                     // counted tokens, two segments in turn
+  __shared__ float sl[kFwdWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % L;
+  const Ring ring(bsm + ((kFwdWarps + 1) * E + 3) / 4 * 4 + warp * Ring::kTotal, a, lane);
   const bool alone = gridDim.x == 1;
   pdl_launch_dependents();
   const int t0 = min((int)((int64_t)blockIdx.x * a.chunk), a.T), t1 = min(t0 + a.chunk, a.T);
   if (blockIdx.x == 0 && !alone)
-    for (int s = tid; s < a.S; s += kBalThreads) a.ticket[s] = 0u;
-  for (int e = tid; e < E; e += kBalThreads) sc[e] = 0;
+    for (int s = tid; s < a.S; s += kFwdThreads) a.ticket[s] = 0u;
+  for (int e = tid; e < E; e += kFwdThreads) sc[e] = 0;
   if (tid < 2) sn[tid] = 0;
   const Segments sg = load_segments(a, tab);
   const int s0 = alone ? 0 : sg.of(t0);
@@ -148,60 +222,63 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_fwd(const BalanceArgs a
       if (sg.at(s) >= t1) break;
       if (b0 >= b1) continue;  // empty, or none of its tokens here: its slot is never read
     }
-    float acc[NI];
+    f32x2 acc[NV / 2];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) acc[i] = 0.0f;
-    int n = 0;
-    float nx[U][NI];
-    int ne[U];   // this lane's expert of each row, -1: none
-    bool nv[U];  // the row counts
-    auto load = [&](int t) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int tu = t + u * kBalWarps;
-        nv[u] = tu < b1 && (a.valid == nullptr || a.valid[tu] != 0);
-        ne[u] = tu < b1 && lane < a.k ? a.idx[(size_t)tu * a.k + lane] : -1;
-        if (tu < b1) load_row<NI, VEC>(a.logits + (size_t)tu * E, E, lane, nx[u]);
+    for (int i = 0; i < NV / 2; ++i) acc[i] = 0ull;
+    // tw: the warp's first row of a turn, t: this lane's
+    int n = 0, slot = 0, tw = b0 + warp * kRows, t = tw + lane / L;
+    for (int u = 0; u < R; ++u) ring.issue(u, t + u * kTurn, t + u * kTurn < b1);
+    bool next_ok = t < b1 && (a.valid == nullptr || a.valid[t] != 0);
+    for (; tw < b1; tw += kTurn, t += kTurn) {
+      f32x2 v[NV / 2];
+      const float *more = ring.take(slot, v);
+      const bool counts = next_ok;
+      next_ok = t + kTurn < b1 && (a.valid == nullptr || a.valid[t + kTurn] != 0);
+      if (counts) {
+        for (int j = sub; j < a.k; j += L) {
+          const int x = __float_as_int(more[j]);
+          if (x >= 0 && x < E) atomicAdd(sc + x, 1);
+        }
+        if (sub == 0) ++n;
       }
-    };
-    int t = b0 + warp;
-    load(t);
-    while (t < b1) {
-      float v[U][NI];
-      int e[U];
-      bool ok[U];
+      __syncwarp();
+      // rows behind b1 are empty copies: every turn waits for one of its own
+      ring.issue(slot, t + R * kTurn, t + R * kTurn < b1);
+      slot = slot + 1 == R ? 0 : slot + 1;
+      float inv;
+      softmax_row<L, NV>(v, inv);
+      // a row that does not count may hold anything: its values are not used
+      if (counts) {
+        const f32x2 i2 = pack2(inv, inv);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        e[u] = ne[u];
-        ok[u] = nv[u];
-#pragma unroll
-        for (int i = 0; i < NI; ++i) v[u][i] = nx[u][i];
-      }
-      t += U * kBalWarps;
-      if (t < b1) load(t);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (!ok[u]) continue;
-        if (e[u] >= 0 && e[u] < E) atomicAdd(sc + e[u], 1);
-        softmax_row<NI>(v[u]);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) acc[i] += v[u][i];
-        ++n;
+        for (int i = 0; i < NV / 2; ++i) acc[i] = fma2(v[i], i2, acc[i]);
       }
     }
+    cp_async_wait<0>();  // the next segment starts its ring anew
+    // the rows' lanes of the warp, then the warps
+#pragma unroll
+    for (int i = 0; i < NV / 2; ++i) {
+      float2 p = unpack2(acc[i]);
+#pragma unroll
+      for (int off = L; off < 32; off <<= 1) {
+        p.x += __shfl_xor_sync(0xffffffffu, p.x, off);
+        p.y += __shfl_xor_sync(0xffffffffu, p.y, off);
+      }
+      const int e0 = expert_of<L, VEC>(2 * i, sub), e1 = expert_of<L, VEC>(2 * i + 1, sub);
+      if (lane < L) {
+        if (e0 < E) sp[warp * E + e0] = p.x;
+        if (e1 < E) sp[warp * E + e1] = p.y;
+      }
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0 && n) atomicAdd(sn + par, n);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int e = expert_of<VEC>(i, lane);
-      if (e < E) sp[warp * E + e] = acc[i];
-    }
     __syncthreads();
     n = sn[par];
     float lsum = 0.0f;
-    for (int e = tid; e < E; e += kBalThreads) {
+    for (int e = tid; e < E; e += kFwdThreads) {
       float p = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kBalWarps; ++w) p += sp[w * E + e];
+      for (int w = 0; w < kFwdWarps; ++w) p += sp[w * E + e];
       if (alone) {
         lsum += finish_expert(a, s, e, p, sc[e], n);
       } else {
@@ -217,14 +294,13 @@ __global__ void __launch_bounds__(kBalThreads) k_balance_fwd(const BalanceArgs a
       else a.part_n[blockIdx.x + s] = n;
     }
     if (alone) {
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) lsum += __shfl_xor_sync(0xffffffffu, lsum, off);
+      lsum = row_add<32>(lsum);
       if (lane == 0) sl[warp] = lsum;
     }
     __syncthreads();
     if (alone && tid == 0) {
       float l = 0.0f;
-      for (int w = 0; w < kBalWarps; ++w) l += sl[w];
+      for (int w = 0; w < kFwdWarps; ++w) l += sl[w];
       a.loss[s] = l;
     }
     par ^= 1;
@@ -295,50 +371,41 @@ __global__ void __launch_bounds__(1024) k_balance_join(const BalanceArgs a) {
   }
 }
 
-// Warps take runs of consecutive tokens, so that f of the segment stays in
-// registers.  The kept part goes through a row of shared memory per warp that
-// is zero between tokens.
-template <int NI, int VEC>
-__global__ void __launch_bounds__(256) k_balance_bwd(const BalanceArgs a) {
-  extern __shared__ float bsm[];
+// The CTA's consecutive tokens go to its warps in turns; a row's lanes keep f of
+// its segment in registers.  The kept part (DW) is added in the row's own place
+// in the ring, where the gradient passes on its way out.
+template <int L, int NV, int VEC, bool DW>
+__global__ void __launch_bounds__(kBwdThreads) k_balance_bwd(const BalanceArgs a) {
+  extern __shared__ __align__(16) float bsm[];
+  using Ring = RowRing<L, NV, VEC, DW>;
+  constexpr int R = Ring::R, kRows = Ring::kRows, kTurn = kBwdWarps * kRows;
   const int E = a.E;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane % L, grp = lane / L;
   __shared__ int32_t tab[kSegTab];
-  float *kept = bsm + (size_t)warp * ((E + 3) & ~3);
-  if (a.dw != nullptr)
-    for (int e = lane; e < E; e += 32) kept[e] = 0.0f;
+  const Ring ring(bsm + warp * Ring::kTotal, a, lane);
+  const int t0 = (int)min((int64_t)a.T, (int64_t)blockIdx.x * a.chunk), t1 = min(t0 + a.chunk, a.T);
+  int slot = 0, tw = t0 + warp * kRows, t = tw + grp;
+  for (int u = 0; u < R; ++u) ring.issue(u, t + u * kTurn, t + u * kTurn < t1);
   const Segments sg = load_segments(a, tab);
-  const int64_t w = (int64_t)blockIdx.x * 8 + warp;
-  const int t0 = (int)min((int64_t)a.T, w * a.chunk), t1 = min(t0 + a.chunk, a.T);
-  if (t0 >= t1) return;
   int s = -1, s_end = t0, s_begin = t0;  // the segment whose f is held; tokens s_begin .. s_end
-  float f[NI], cs = 0.0f;
+  f32x2 f[NV / 2];
+  float cs = 0.0f;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) f[i] = 0.0f;
-  // the next row and its pairs are on their way while a row is worked on
-  float nx[NI], nw = 0.0f, nd = 0.0f;
-  int ne = -1;
-  bool nv = true;
-  auto load = [&](int t) {
-    load_row<NI, VEC>(a.logits + (size_t)t * E, E, lane, nx);
-    if (a.valid != nullptr) nv = a.valid[t] != 0;
-    if (a.dw != nullptr && lane < a.k) {
-      const size_t at = (size_t)t * a.k + lane;
-      ne = a.idx[at];
-      nw = a.w[at];
-      nd = a.dw[at];
+  for (int i = 0; i < NV / 2; ++i) f[i] = 0ull;
+  bool next_ok = t < t1 && (a.valid == nullptr || a.valid[t] != 0);
+  for (; tw < t1; tw += kTurn, t += kTurn) {
+    f32x2 o[NV / 2];
+    float *more = ring.take(slot, o);
+    const bool valid = next_ok, in = t < t1;
+    next_ok = t + kTurn < t1 && (a.valid == nullptr || a.valid[t + kTurn] != 0);
+    int x = -1;
+    float wi = 0.0f, di = 0.0f;  // this lane's pair (the first of several where k > L)
+    if (DW && in && sub < a.k) {
+      x = __float_as_int(more[sub]);
+      wi = more[32 + sub];
+      di = more[64 + sub];
     }
-  };
-  load(t0);
-  for (int t = t0; t < t1; ++t) {
-    float v[NI];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) v[i] = nx[i];
-    const int e = ne;
-    const float wi = nw, di = nd;
-    const bool valid = nv;
-    if (t + 1 < t1) load(t + 1);
-    if (t >= s_end) {
+    if (t >= s_end && in) {
       s = sg.of(t);
       s_begin = s < a.S ? sg.at(s) : a.T;
       s_end = s < a.S ? sg.at(s + 1) : a.T;
@@ -346,64 +413,96 @@ __global__ void __launch_bounds__(256) k_balance_bwd(const BalanceArgs a) {
       cs = n > 0 ? __fdiv_rn(a.dloss[s], (float)n) : 0.0f;
       const float fs = n > 0 ? (float)((double)E / ((double)a.k * n)) : 0.0f;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int e = expert_of<VEC>(i, lane);
-        f[i] = n > 0 && e < E ? (float)a.counts[(size_t)s * E + e] * fs : 0.0f;
+      for (int i = 0; i < NV / 2; ++i) {
+        const int e0 = expert_of<L, VEC>(2 * i, sub), e1 = expert_of<L, VEC>(2 * i + 1, sub);
+        const int *c = a.counts + (size_t)s * E;
+        f[i] = pack2(n > 0 && e0 < E ? (float)c[e0] * fs : 0.0f, n > 0 && e1 < E ? (float)c[e1] * fs : 0.0f);
       }
     }
-    const bool counted = t >= s_begin && s < a.S && valid;
-    if (counted) {
-      softmax_row<NI>(v);
-      float dot = 0.0f;
+    __syncwarp();
+    float inv;
+    softmax_row<L, NV>(o, inv);
+    f32x2 dot2 = 0ull;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) dot = ffma(f[i], v[i], dot);
+    for (int i = 0; i < NV / 2; ++i) dot2 = fma2(f[i], o[i], dot2);
+    const float2 h = unpack2(dot2);
+    const float dot = row_add<L>(h.x + h.y) * inv;
+    if (t >= s_begin && s < a.S && valid) {
+      const float c = cs * inv;
+      const f32x2 nd = pack2(-dot, -dot), c2 = pack2(c, c);
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-#pragma unroll
-      for (int i = 0; i < NI; ++i) v[i] = cs * v[i] * (f[i] - dot);
+      for (int i = 0; i < NV / 2; ++i) o[i] = mul2(mul2(o[i], c2), add2(f[i], nd));
     } else {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) v[i] = 0.0f;
+      for (int i = 0; i < NV / 2; ++i) o[i] = 0ull;
     }
-    if (a.dw != nullptr) {
-      float wd = wi * di;
+    if (DW) {
+      float *grad = more - Ring::kCols;
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) wd += __shfl_xor_sync(0xffffffffu, wd, off);
-      const bool live = e >= 0 && e < E;
-      const float g = wi * (di - wd);
-      const unsigned same = __match_any_sync(0xffffffffu, live ? e : -1 - lane);
-      if (__any_sync(0xffffffffu, same & (same - 1))) {
+      for (int i = 0; i < NV; i += VEC == 4 ? 4 : 2) {
+        const int e = expert_of<L, VEC>(i, sub);
+        if (VEC == 4) {
+          if (e < E) *reinterpret_cast<ulonglong2 *>(grad + e) = make_ulonglong2(o[i / 2], o[i / 2 + 1]);
+        } else {
+          const float2 p = unpack2(o[i / 2]);
+          if (e < E) grad[e] = p.x;
+          if (e + L < E) grad[e + L] = p.y;
+        }
+      }
+      __syncwarp();
+      if (a.k <= L) {
+        const float wd = row_add<L>(wi * di);
+        const bool live = x >= 0 && x < E;
+        const float g = wi * (di - wd);
         // an expert listed twice: its terms one after the other, by slot
-        for (int i = 0; i < a.k; ++i) {
-          if (lane == i && live) kept[e] += g;
+        const unsigned same = __match_any_sync(0xffffffffu, live ? grp * MOE_MAX_E + x : -1 - lane);
+        if (__any_sync(0xffffffffu, same & (same - 1))) {
+          for (int j = 0; j < a.k; ++j) {
+            if (sub == j && live) grad[x] += g;
+            __syncwarp();
+          }
+        } else if (live) {
+          grad[x] += g;
+        }
+      } else {
+        float wd = 0.0f;
+        for (int j = sub; j < a.k && in; j += L) wd = ffma(more[32 + j], more[64 + j], wd);
+        wd = row_add<L>(wd);
+        for (int j = 0; j < a.k; ++j) {
+          if (sub == j % L && in) {
+            const int xj = __float_as_int(more[j]);
+            if (xj >= 0 && xj < E) grad[xj] += more[32 + j] * (more[64 + j] - wd);
+          }
           __syncwarp();
         }
-      } else if (live) {
-        kept[e] = g;
       }
       __syncwarp();
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int x = expert_of<VEC>(i, lane);
-        if (x < E) v[i] += kept[x];
+      for (int i = 0; i < NV; i += VEC == 4 ? 4 : 2) {
+        const int e = expert_of<L, VEC>(i, sub);
+        if (VEC == 4) {
+          const ulonglong2 q = e < E ? *reinterpret_cast<const ulonglong2 *>(grad + e) : make_ulonglong2(0ull, 0ull);
+          o[i / 2] = q.x, o[i / 2 + 1] = q.y;
+        } else {
+          o[i / 2] = pack2(e < E ? grad[e] : 0.0f, e + L < E ? grad[e + L] : 0.0f);
+        }
       }
-      __syncwarp();
-      if (live) kept[e] = 0.0f;
-      __syncwarp();
     }
+    __syncwarp();
+    ring.issue(slot, t + R * kTurn, t + R * kTurn < t1);
+    slot = slot + 1 == R ? 0 : slot + 1;
+    if (!in) continue;
     float *row = a.dlogits + (size_t)t * E;
-    if (VEC == 4) {
 #pragma unroll
-      for (int j = 0; j < NI / 4; ++j) {
-        const int e = j * 128 + lane * 4;
-        if (e < E)
-          __stcs(reinterpret_cast<float4 *>(row + e), make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int e = i * 32 + lane;
-        if (e < E) __stcs(row + e, v[i]);
+    for (int i = 0; i < NV; i += VEC == 4 ? 4 : 2) {
+      const int e0 = expert_of<L, VEC>(i, sub);
+      const float2 p = unpack2(o[i / 2]);
+      if (VEC == 4) {
+        const float2 q = unpack2(o[i / 2 + 1]);
+        if (e0 < E) __stcs(reinterpret_cast<float4 *>(row + e0), make_float4(p.x, p.y, q.x, q.y));
+      } else {
+        if (e0 < E) __stcs(row + e0, p.x);
+        if (e0 + L < E) __stcs(row + e0 + L, p.y);
       }
     }
   }
@@ -414,35 +513,47 @@ bool vec4(const BalanceArgs &a) {
   return a.E % 4 == 0 && (p & 15) == 0;
 }
 
-template <int NI, int VEC>
+template <int L, int NV, int VEC>
 cudaError_t fwd(const BalanceArgs &a, int grid, cudaStream_t s) {
-  const size_t smem = (size_t)(kBalWarps + 1) * a.E * 4;
+  const size_t smem = ((size_t)((kFwdWarps + 1) * a.E + 3) / 4 * 4 + kFwdWarps * RowRing<L, NV, VEC, false>::kTotal) * 4;
   static int smem_set[64] = {0};
-  cudaError_t err = ensure_smem(k_balance_fwd<NI, VEC>, smem, smem_set);
+  cudaError_t err = ensure_smem(k_balance_fwd<L, NV, VEC>, smem, smem_set);
   if (err != cudaSuccess) return err;
-  k_balance_fwd<NI, VEC><<<grid, kBalThreads, smem, s>>>(a);
+  k_balance_fwd<L, NV, VEC><<<grid, kFwdThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
-template <int NI, int VEC>
+template <int L, int NV, int VEC, bool DW>
+cudaError_t bwd_dw(BalanceArgs a, int grid, cudaStream_t s) {
+  using Ring = RowRing<L, NV, VEC, DW>;
+  const size_t smem = (size_t)kBwdWarps * Ring::kTotal * 4;
+  static int smem_set[64] = {0};
+  cudaError_t err = ensure_smem(k_balance_bwd<L, NV, VEC, DW>, smem, smem_set);
+  if (err != cudaSuccess) return err;
+  if (!DW) a.idx = nullptr;  // not read
+  k_balance_bwd<L, NV, VEC, DW><<<grid, kBwdThreads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int L, int NV, int VEC>
 cudaError_t bwd(const BalanceArgs &a, int grid, cudaStream_t s) {
-  const size_t smem = a.dw != nullptr ? (size_t)8 * ((a.E + 3) & ~3) * 4 : 0;
-  k_balance_bwd<NI, VEC><<<grid, 256, smem, s>>>(a);
-  return cudaGetLastError();
+  return a.dw != nullptr ? bwd_dw<L, NV, VEC, true>(a, grid, s) : bwd_dw<L, NV, VEC, false>(a, grid, s);
 }
 
-// Values per lane: the smallest instance that holds the row.
-#define MOE_BALANCE_DISPATCH(fn)                                              \
-  if (vec4(a)) {                                                             \
-    if (a.E <= 128) return fn<4, 4>(a, grid, s);                             \
-    if (a.E <= 256) return fn<8, 4>(a, grid, s);                             \
-    if (a.E <= 512) return fn<16, 4>(a, grid, s);                            \
-    return fn<32, 4>(a, grid, s);                                            \
-  }                                                                          \
-  if (a.E <= 128) return fn<4, 1>(a, grid, s);                               \
-  if (a.E <= 256) return fn<8, 1>(a, grid, s);                               \
-  if (a.E <= 512) return fn<16, 1>(a, grid, s);                              \
-  return fn<32, 1>(a, grid, s);
+// Lanes per row and values per lane: the smallest instance that holds the row.
+#define MOE_BALANCE_DISPATCH(fn)                    \
+  if (vec4(a)) {                                   \
+    if (a.E <= 64) return fn<8, 8, 4>(a, grid, s);   \
+    if (a.E <= 128) return fn<8, 16, 4>(a, grid, s); \
+    if (a.E <= 256) return fn<8, 32, 4>(a, grid, s); \
+    if (a.E <= 512) return fn<16, 32, 4>(a, grid, s); \
+    return fn<32, 32, 4>(a, grid, s);              \
+  }                                                \
+  if (a.E <= 64) return fn<8, 8, 1>(a, grid, s);     \
+  if (a.E <= 128) return fn<8, 16, 1>(a, grid, s);   \
+  if (a.E <= 256) return fn<8, 32, 1>(a, grid, s);   \
+  if (a.E <= 512) return fn<16, 32, 1>(a, grid, s);  \
+  return fn<32, 32, 1>(a, grid, s);
 
 cudaError_t dispatch_fwd(const BalanceArgs &a, int grid, cudaStream_t s) { MOE_BALANCE_DISPATCH(fwd) }
 cudaError_t dispatch_bwd(const BalanceArgs &a, int grid, cudaStream_t s) { MOE_BALANCE_DISPATCH(bwd) }
@@ -481,13 +592,12 @@ cudaError_t launch_balance_fwd(const BalanceArgs &a, int grid, cudaStream_t s) {
 }
 
 cudaError_t launch_balance_bwd(const BalanceArgs &a, int sms, cudaStream_t s) {
-  // eight CTAs of eight warps fill an SM; a warp's run of tokens is what is left
+  // a turn of 32 rows per CTA (8 lanes a row) at least, two waves of two CTAs per SM
   BalanceArgs b = a;
-  const int64_t warps = (int64_t)sms * 64;
-  b.chunk = (int)((a.T + warps - 1) / warps);
-  if (b.chunk < 1) b.chunk = 1;
-  const int nw = (a.T + b.chunk - 1) / b.chunk;
-  return dispatch_bwd(b, (nw + 7) / 8, s);
+  const int64_t most = (int64_t)sms * 4;
+  b.chunk = (int)((a.T + most - 1) / most);
+  b.chunk = b.chunk < 8 ? 8 : (b.chunk + 31) / 32 * 32;
+  return dispatch_bwd(b, (a.T + b.chunk - 1) / b.chunk, s);
 }
 
 }  // namespace moe
