@@ -209,6 +209,12 @@ __global__ void __launch_bounds__(kFwdThreads) k_balance_fwd(const BalanceArgs a
   const bool alone = gridDim.x == 1;
   pdl_launch_dependents();
   const int t0 = min((int)((int64_t)blockIdx.x * a.chunk), a.T), t1 = min(t0 + a.chunk, a.T);
+  // the first rows are brought near while the segments are looked up
+  {
+    const int64_t bytes = (int64_t)min(t1 - t0, kTurn) * E * 4;
+    for (int64_t o = (int64_t)tid * 128; o < bytes; o += kFwdThreads * 128)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const char *>(a.logits + (size_t)t0 * E) + o) : "memory");
+  }
   if (blockIdx.x == 0 && !alone)
     for (int s = tid; s < a.S; s += kFwdThreads) a.ticket[s] = 0u;
   for (int e = tid; e < E; e += kFwdThreads) sc[e] = 0;

@@ -313,7 +313,7 @@ struct BalanceArgs {
   const float *dloss, *w, *dw;  // backward: [S], [T][k] or null, [T][k] or null
   float *dlogits;          // [T][E]
 };
-constexpr int kBalanceChunkMin = 32;  // tokens a CTA of the forward takes at least,
+constexpr int kBalanceChunkMin = 16;  // tokens a CTA of the forward takes at least,
 constexpr int kBalanceCtas = 2;       // and CTAs per SM at most
 // CTAs and tokens per CTA of the forward.
 struct BalancePlan {

@@ -458,7 +458,7 @@ struct ShrinkStep {
 };
 
 template <int RT, bool BF16, bool TR>
-__global__ void __launch_bounds__(256) k_lora_shrink(const LoraArgs a, const float *src, int L, const void *M,
+__global__ void __launch_bounds__(256, 2) k_lora_shrink(const LoraArgs a, const float *src, int L, const void *M,
                                                      float *dst, float *user) {
   extern __shared__ __align__(16) float red[];  // [8][16][RT * 8]
   namespace cg = cooperative_groups;

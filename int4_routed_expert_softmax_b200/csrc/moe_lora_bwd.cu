@@ -41,26 +41,55 @@ __device__ __forceinline__ float pow2_to_15(float m) {
 // ===========================================================================
 // dA, dB: D[j][l] = sum over the adapter's tokens of left[p][j] right[t][l].
 // left: fp32 rows of r by position (or by token, `left_by_token`, then times
-// scale_a); right: fp32 rows of L by token.  A warp holds 32 columns l (a lane
-// reads four consecutive ones for four MMA tiles) by up to 64 rows j, and
-// takes every fourth step of 8 tokens; the four warps of a column block are
-// joined in shared memory in a fixed order.  out is [n][r][L], or [n][L][r]
-// if `l_major`.
+// scale_a); right: fp32 rows of L by token.  A CTA takes 16 RM rows j by 64
+// columns l of one adapter; its tokens come 32 at a time through three stages
+// of shared memory (cp.async; rows padded to 72 words keep the fragments' reads
+// free of bank conflicts).  A warp holds 32 columns (a lane reads four
+// consecutive ones for four MMA tiles) by all rows, and takes 8 tokens of a
+// stage; the four warps of a column block are joined in a fixed order.  out is
+// [n][r][L], or [n][L][r] if `l_major`.
 // ===========================================================================
-constexpr int kOuterL = 64;  // columns per CTA (two blocks of 32)
-constexpr int kOuterJ = 64;  // rows per CTA
+constexpr int kOuterL = 64, kOuterJ = 64, kOuterT = 32;  // columns, rows at most, tokens per stage
+constexpr int kOuterRow = 72;                            // words of a row in shared memory
+constexpr int kOuterStages = 3;
+constexpr int kOuterStage = 2 * kOuterT * kOuterRow;     // words: left rows, right rows
+constexpr size_t kOuterSmem = (size_t)kOuterStages * kOuterStage * 4;
+static_assert(3 * 2 * 32 * 17 <= kOuterStages * kOuterStage, "the join fits the stages");
+
+// 16-byte asynchronous copy; src_bytes = 0 writes zeros.
+__device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16u : 0u)
+               : "memory");
+}
 
 template <int RM>
-__global__ void __launch_bounds__(256) k_lora_outer(const LoraArgs a, const float *left, int left_by_token,
-                                                    const float *right, int L, float *out, int l_major) {
-  __shared__ float red[3][2][32][33];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+__global__ void __launch_bounds__(256, 2) k_lora_outer(const LoraArgs a, const float *left, int left_by_token,
+                                                       const float *right, int L, float *out, int l_major) {
+  extern __shared__ __align__(16) float osm[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int id = blockIdx.y, r = a.r;
-  const int lb = blockIdx.x * kOuterL + (warp & 1) * 32, j0 = blockIdx.z * kOuterJ, tw = warp >> 1;
-  const int p0 = a.off[id], p1 = a.off[id + 1];
-  const int l = lb + 4 * g;
-  const bool in = l < L;  // L % 8 == 0
+  const int l0 = blockIdx.x * kOuterL, lb = l0 + (warp & 1) * 32, j0 = blockIdx.z * kOuterJ, tw = warp >> 1;
+  const int p0 = a.off[id], p1 = a.off[id + 1], steps = (p1 - p0 + kOuterT - 1) / kOuterT;
   const float sc = left_by_token ? a.scale[id] : 1.0f;
+  // this thread's copies of a stage: row tid / 8, 16-byte pieces tid % 8 and + 8 of both sides
+  const int crow = tid >> 3, piece = tid & 7;
+  auto token = [&](int st) {
+    const int p = p0 + st * kOuterT + crow;
+    return p < p1 ? a.perm[p] : -1;
+  };
+  auto load = [&](int st, int t) {
+    float *b = osm + (st % kOuterStages) * kOuterStage + crow * kOuterRow;
+    const bool in = t >= 0;
+    const float *lr = left + (size_t)(in ? (left_by_token ? t : p0 + st * kOuterT + crow) : 0) * r + j0;
+    const float *rr = right + (size_t)(in ? t : 0) * L + l0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = (piece + 8 * h) * 4;
+      // columns behind r or L are left as they are: no stored sum sees them
+      if (c < RM * 16 && j0 + c < r) cp_async16_or_zero(b + c, lr + c, in);
+      if (l0 + c < L) cp_async16_or_zero(b + kOuterT * kOuterRow + c, rr + c, in);
+    }
+  };
   float acc[RM][4][4];
 #pragma unroll
   for (int m = 0; m < RM; ++m)
@@ -68,14 +97,21 @@ __global__ void __launch_bounds__(256) k_lora_outer(const LoraArgs a, const floa
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[m][i][c] = 0.0f;
-  for (int p = p0 + 8 * tw; p < p1; p += 32) {
-    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const int pa = p + q, pb = p + q + 4;
-    const bool va = pa < p1, vb = pb < p1;
-    const int ta = va ? a.perm[pa] : 0, tb = vb ? a.perm[pb] : 0;
-    const float4 xa = va && in ? *reinterpret_cast<const float4 *>(right + (size_t)ta * L + l) : zero;
-    const float4 xb = vb && in ? *reinterpret_cast<const float4 *>(right + (size_t)tb * L + l) : zero;
-    const float *la = left + (size_t)(left_by_token ? ta : pa) * r, *lo_ = left + (size_t)(left_by_token ? tb : pb) * r;
+#pragma unroll
+  for (int st = 0; st < kOuterStages - 1; ++st) {
+    if (st < steps) load(st, token(st));
+    cp_async_commit();
+  }
+  int tn = token(kOuterStages - 1);  // one stage ahead of its copies
+  for (int st = 0; st < steps; ++st) {
+    cp_async_wait<kOuterStages - 2>();
+    __syncthreads();
+    if (st + kOuterStages - 1 < steps) load(st + kOuterStages - 1, tn);
+    cp_async_commit();
+    tn = token(st + kOuterStages);
+    const float *b = osm + (st % kOuterStages) * kOuterStage + (tw * 8 + q) * kOuterRow;
+    const float *rb = b + kOuterT * kOuterRow + (warp & 1) * 32 + 4 * g;
+    const float4 xa = *reinterpret_cast<const float4 *>(rb), xb = *reinterpret_cast<const float4 *>(rb + 4 * kOuterRow);
     const float fa[4] = {xa.x, xa.y, xa.z, xa.w}, fb[4] = {xb.x, xb.y, xb.z, xb.w};
     Tf32Pair ba[4], bb[4];
 #pragma unroll
@@ -85,12 +121,12 @@ __global__ void __launch_bounds__(256) k_lora_outer(const LoraArgs a, const floa
     }
 #pragma unroll
     for (int m = 0; m < RM; ++m) {
-      const int j = j0 + m * 16 + g;
+      const float *lp = b + m * 16 + g;
       Tf32Pair e[4];
-      e[0] = split_tf32(va && j < r ? sc * la[j] : 0.0f);
-      e[1] = split_tf32(va && j + 8 < r ? sc * la[j + 8] : 0.0f);
-      e[2] = split_tf32(vb && j < r ? sc * lo_[j] : 0.0f);
-      e[3] = split_tf32(vb && j + 8 < r ? sc * lo_[j + 8] : 0.0f);
+      e[0] = split_tf32(sc * lp[0]);
+      e[1] = split_tf32(sc * lp[8]);
+      e[2] = split_tf32(sc * lp[4 * kOuterRow]);
+      e[3] = split_tf32(sc * lp[4 * kOuterRow + 8]);
       const uint32_t hi[4] = {e[0].hi, e[1].hi, e[2].hi, e[3].hi}, lw[4] = {e[0].lo, e[1].lo, e[2].lo, e[3].lo};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -102,23 +138,28 @@ __global__ void __launch_bounds__(256) k_lora_outer(const LoraArgs a, const floa
       }
     }
   }
-  // join the four token shares, 16 rows at a time (a lane's 16 sums as a row of red)
+  cp_async_wait<0>();
+  // join the four token shares, 16 rows at a time (a lane's 16 sums as a row of 17 words)
 #pragma unroll
   for (int m = 0; m < RM; ++m) {
     __syncthreads();
     if (tw > 0) {
+      float *o = osm + (((tw - 1) * 2 + (warp & 1)) * 32 + lane) * 17;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) red[tw - 1][warp & 1][lane][4 * i + c] = acc[m][i][c];
+        for (int c = 0; c < 4; ++c) o[4 * i + c] = acc[m][i][c];
     }
     __syncthreads();
     if (tw == 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int w = 0; w < 3; ++w) {
+        const float *o = osm + ((w * 2 + (warp & 1)) * 32 + lane) * 17;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          for (int w = 0; w < 3; ++w) acc[m][i][c] += red[w][warp & 1][lane][4 * i + c];
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[m][i][c] += o[4 * i + c];
+      }
       // acc[m][i]: rows g, g + 8, columns 4 * 2q + i and 4 * (2q + 1) + i of the block
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -399,7 +440,10 @@ template <int RM>
 cudaError_t outer_rows(const LoraArgs &a, const float *left, int by_token, const float *right, int L, float *out,
                        int l_major, cudaStream_t s) {
   const dim3 grid((unsigned)((L + kOuterL - 1) / kOuterL), (unsigned)a.n, (unsigned)((a.r + kOuterJ - 1) / kOuterJ));
-  k_lora_outer<RM><<<grid, 256, 0, s>>>(a, left, by_token, right, L, out, l_major);
+  static int smem_set[64] = {0};
+  const cudaError_t err = ensure_smem(k_lora_outer<RM>, kOuterSmem, smem_set);
+  if (err != cudaSuccess) return err;
+  k_lora_outer<RM><<<grid, 256, kOuterSmem, s>>>(a, left, by_token, right, L, out, l_major);
   return cudaGetLastError();
 }
 
