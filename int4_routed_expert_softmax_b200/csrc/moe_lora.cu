@@ -366,7 +366,8 @@ __device__ void sort_tokens(const LoraArgs &a, int *tab, int warps) {
 }
 
 // The first kernel of a sorted call.  CTA 0 sorts the tokens by adapter; the
-// others (where `operands`) lay out the base product's operands: x^ over a scale
+// others take the powers of two of W's rows if `a.wexp` (the backward), else,
+// if there are any, they lay out the base product's operands: x^ over a scale
 // of each 64-group (a warp: 512 inputs of a token), W's integers, exact in fp16
 // (a warp: 1024 packed bytes), and in fp32 the scales of both, transposed.
 __global__ void __launch_bounds__(1024) k_lora_prep(const LoraArgs a, int warps) {
@@ -375,6 +376,22 @@ __global__ void __launch_bounds__(1024) k_lora_prep(const LoraArgs a, int warps)
   if (blockIdx.x == 0) {
     if (threadIdx.x < 4) a.status[threadIdx.x] = 0;
     sort_tokens(a, tab, warps);
+    return;
+  }
+  if (a.wexp != nullptr) {
+    // wexp[n]: what brings the row's largest value near 2^15; wexp[N + n]: its inverse
+    const int n = (int)(blockIdx.x - 1) * 32 + (threadIdx.x >> 5), ln = threadIdx.x & 31, Gn = a.K / 64;
+    if (n >= a.N) return;
+    const __half *sc = reinterpret_cast<const __half *>(a.W + (size_t)a.N * (a.K / 2)) + (size_t)n * Gn;
+    float m = 0.0f;
+    for (int g = ln; g < Gn; g += 32) m = fmaxf(m, fabsf(__half2float(sc[g])));
+    m = warp_max(m);
+    if (ln == 0) {
+      const float e = pow2_to_15(8.0f * m);
+      a.wexp[n] = e;
+      // a row of zeros must not set the power of two of g's rows
+      a.wexp[a.N + n] = m == 0.0f ? 0.0f : 1.0f / e;
+    }
     return;
   }
   const int lane = threadIdx.x & 31, per = (a.K + 511) / 512, G = a.K / 64;
@@ -819,119 +836,126 @@ __global__ void __launch_bounds__(kBaseThreads, 1) k_lora_base(const LoraArgs a,
 }
 
 // dst[t][l] += sum_j s[p][j] M_a(j, l): M_a(j, l) = A_a[j][l], or B_a[l][j] if
-// LM.  A CTA takes up to 16 tokens of one adapter (the MMA's rows) by 256
-// columns, a warp 32: four MMA tiles.  With M = A a lane's column of the four
-// tiles are four consecutive l (one 8-byte load per row j), with M = B a lane
-// reads two consecutive j of each column.  The loads of 32 of the rank are
-// issued together.
+// LM.  A CTA takes up to 16 tokens of one adapter (the MMA's rows) by `cols`
+// columns, 256 at a time, a warp 32 of them: four MMA tiles.  The tokens' factors
+// are split into tf32 hi + lo once, in shared memory as the MMAs' operands.
+// With M = A a lane's column of the four tiles are four consecutive l (one
+// 8-byte load per row j), with M = B a lane reads two consecutive j of each
+// column.  The loads of 32 of the rank are issued together.
 template <bool BF16, bool LM>
-__global__ void __launch_bounds__(256) k_lora_expand(const LoraArgs a, const float *s, const void *M, int L,
-                                                     float *dst) {
+__global__ void __launch_bounds__(256, 2) k_lora_expand(const LoraArgs a, const float *s, const void *M, int L,
+                                                        float *dst, int cols) {
+  __shared__ __align__(16) uint32_t frag[kLoraMaxRank / 8][32][8];  // [8 of the rank][lane][hi, lo]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int r = a.r, lb = blockIdx.y * 256 + warp * 32;
+  const int r = a.r, l_end = min(L, (int)(blockIdx.y + 1) * cols);
   pdl_wait();
-  if ((int)blockIdx.x >= a.tile[a.n + 1] || lb >= L) return;
+  if ((int)blockIdx.x >= a.tile[a.n + 1]) return;
   const int id = adapter_at(a.tile, a.n, blockIdx.x);
   if (id == a.n) return;
   const int p0 = a.off[id] + ((int)blockIdx.x - a.tile[id]) * kLoraSeg;
   const int np = min(kLoraSeg, a.off[id + 1] - p0);
   const uint16_t *Ma = static_cast<const uint16_t *>(M) + (size_t)id * r * L;
   const bool in0 = g < np, in1 = g + 8 < np;
-  const float *v0 = s + (size_t)(p0 + g) * r, *v1 = s + (size_t)(p0 + g + 8) * r;
-  // this lane's outputs: LM: columns lb + 8 i + 2q, + 1 of tile i; else lb + 8q .. + 7
-  const int lo = LM ? lb + 2 * q : lb + 8 * q;
-  float *o0 = dst + (in0 ? (size_t)a.perm[p0 + g] * L : 0) + lo, *o1 = dst + (in1 ? (size_t)a.perm[p0 + g + 8] * L : 0) + lo;
-  float old[2][8];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const bool in = h ? in1 : in0;
-    const float *o = h ? o1 : o0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float2 v = make_float2(0.0f, 0.0f);
-      if (in && (LM ? lo + 8 * i < L : lo < L)) v = *reinterpret_cast<const float2 *>(o + (LM ? 8 * i : 2 * i));
-      old[h][2 * i] = v.x;
-      old[h][2 * i + 1] = v.y;
-    }
+  // LM: a lane's k index q and q + 4 of an MMA are j = 2q, 2q + 1; else j = q, q + 4
+  for (int m = warp; m < r / 8; m += 8) {
+    const int ja = 8 * m + (LM ? 2 * q : q), jb = LM ? ja + 1 : ja + 4;
+    const float *v0 = s + (size_t)(p0 + g) * r, *v1 = v0 + 8 * (size_t)r;
+    const Tf32Pair e[4] = {split_tf32(in0 ? v0[ja] : 0.0f), split_tf32(in1 ? v1[ja] : 0.0f),
+                           split_tf32(in0 ? v0[jb] : 0.0f), split_tf32(in1 ? v1[jb] : 0.0f)};
+    uint4 *f = reinterpret_cast<uint4 *>(frag[m][lane]);
+    f[0] = make_uint4(e[0].hi, e[1].hi, e[2].hi, e[3].hi);
+    f[1] = make_uint4(e[0].lo, e[1].lo, e[2].lo, e[3].lo);
   }
-  float acc[4][4];
+  float *d0 = dst + (in0 ? (size_t)a.perm[p0 + g] * L : 0), *d1 = dst + (in1 ? (size_t)a.perm[p0 + g + 8] * L : 0);
+  __syncthreads();
+  for (int lb = blockIdx.y * cols + warp * 32; lb < l_end; lb += 256) {
+    // this lane's outputs: LM: columns lb + 8 i + 2q, + 1 of tile i; else lb + 8q .. + 7
+    const int lo = LM ? lb + 2 * q : lb + 8 * q;
+    float old[2][8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int h = 0; h < 2; ++h) {
+      const bool in = h ? in1 : in0;
+      const float *o = (h ? d1 : d0) + lo;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
-  for (int j0 = 0; j0 < r; j0 += 32) {
-    // LM: per 8 of j and tile one word (j = 2q, 2q + 1 of column 8 i + g); else per 8 of j two rows (q, q + 4) of 4 columns
-    uint32_t w[4][4];
-    float2 e0[4], e1[4];
+      for (int i = 0; i < 4; ++i) {
+        float2 v = make_float2(0.0f, 0.0f);
+        if (in && (LM ? lo + 8 * i < L : lo < L)) v = *reinterpret_cast<const float2 *>(o + (LM ? 8 * i : 2 * i));
+        old[h][2 * i] = v.x;
+        old[h][2 * i + 1] = v.y;
+      }
+    }
+    float acc[4][4];
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int j = j0 + 8 * m;
-      e0[m] = e1[m] = make_float2(0.0f, 0.0f);
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[m][i] = 0u;
-      if (j < r) {
-        if (LM) {
+      for (int c = 0; c < 4; ++c) acc[i][c] = 0.0f;
+    for (int j0 = 0; j0 < r; j0 += 32) {
+      // LM: per 8 of j and tile one word (j = 2q, 2q + 1 of column 8 i + g); else per 8 of j two rows (q, q + 4) of 4 columns
+      uint32_t w[4][4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (lb + 8 * i < L)
-              w[m][i] = __ldg(reinterpret_cast<const uint32_t *>(Ma + (size_t)(lb + 8 * i + g) * r + j + 2 * q));
-          if (in0) e0[m] = *reinterpret_cast<const float2 *>(v0 + j + 2 * q);
-          if (in1) e1[m] = *reinterpret_cast<const float2 *>(v1 + j + 2 * q);
-        } else {
-          if (lb + 4 * g < L) {
+      for (int m = 0; m < 4; ++m) {
+        const int j = j0 + 8 * m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[m][i] = 0u;
+        if (j < r) {
+          if (LM) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (lb + 8 * i < L)
+                w[m][i] = __ldg(reinterpret_cast<const uint32_t *>(Ma + (size_t)(lb + 8 * i + g) * r + j + 2 * q));
+          } else if (lb + 4 * g < L) {
             const uint2 x = __ldg(reinterpret_cast<const uint2 *>(Ma + (size_t)(j + q) * L + lb + 4 * g));
             const uint2 y = __ldg(reinterpret_cast<const uint2 *>(Ma + (size_t)(j + q + 4) * L + lb + 4 * g));
             w[m][0] = x.x, w[m][1] = x.y, w[m][2] = y.x, w[m][3] = y.y;
           }
-          if (in0) e0[m] = make_float2(v0[j + q], v0[j + q + 4]);
-          if (in1) e1[m] = make_float2(v1[j + q], v1[j + q + 4]);
         }
       }
-    }
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      if (j0 + 8 * m >= r) break;
-      const Tf32Pair x0 = split_tf32(e0[m].x), x1 = split_tf32(e1[m].x), y0 = split_tf32(e0[m].y), y1 = split_tf32(e1[m].y);
-      const uint32_t hi[4] = {x0.hi, x1.hi, y0.hi, y1.hi}, lw[4] = {x0.lo, x1.lo, y0.lo, y1.lo};
-      float fa[4], fb[4];
-      if (LM) {
+      for (int m = 0; m < 4; ++m) {
+        if (j0 + 8 * m >= r) break;
+        const uint4 *f = reinterpret_cast<const uint4 *>(frag[j0 / 8 + m][lane]);
+        const uint4 fh = f[0], fl = f[1];
+        const uint32_t hi[4] = {fh.x, fh.y, fh.z, fh.w}, lw[4] = {fl.x, fl.y, fl.z, fl.w};
+        float fa[4], fb[4];
+        if (LM) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = half2_values<BF16>(w[m][i]);
+            fa[i] = x.x, fb[i] = x.y;
+          }
+        } else {
+          const float2 a0 = half2_values<BF16>(w[m][0]), a1 = half2_values<BF16>(w[m][1]);
+          const float2 b0 = half2_values<BF16>(w[m][2]), b1 = half2_values<BF16>(w[m][3]);
+          fa[0] = a0.x, fa[1] = a0.y, fa[2] = a1.x, fa[3] = a1.y;
+          fb[0] = b0.x, fb[1] = b0.y, fb[2] = b1.x, fb[3] = b1.y;
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 f = half2_values<BF16>(w[m][i]);
-          fa[i] = f.x, fb[i] = f.y;
+          float t[4];
+          mma_tf32_zero(t, lw, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
+          mma_tf32(t, hi, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
+          add4(acc[i], t);
         }
-      } else {
-        const float2 a0 = half2_values<BF16>(w[m][0]), a1 = half2_values<BF16>(w[m][1]);
-        const float2 b0 = half2_values<BF16>(w[m][2]), b1 = half2_values<BF16>(w[m][3]);
-        fa[0] = a0.x, fa[1] = a0.y, fa[2] = a1.x, fa[3] = a1.y;
-        fb[0] = b0.x, fb[1] = b0.y, fb[2] = b1.x, fb[3] = b1.y;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float t[4];
-        mma_tf32_zero(t, lw, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
-        mma_tf32(t, hi, __float_as_uint(fa[i]), __float_as_uint(fb[i]));
-        add4(acc[i], t);
       }
     }
-  }
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (!(h ? in1 : in0)) continue;
-    float *o = h ? o1 : o0;
-    if (LM) {
+    for (int h = 0; h < 2; ++h) {
+      if (!(h ? in1 : in0)) continue;
+      float *o = (h ? d1 : d0) + lo;
+      if (LM) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (lo + 8 * i < L)
-          *reinterpret_cast<float2 *>(o + 8 * i) =
-              make_float2(old[h][2 * i] + acc[i][2 * h], old[h][2 * i + 1] + acc[i][2 * h + 1]);
-    } else if (lo < L) {
-      // columns lo + 0 .. 3 are this lane's first column of tiles 0 .. 3, lo + 4 .. 7 its second
-      float4 *f = reinterpret_cast<float4 *>(o);
-      f[0] = make_float4(old[h][0] + acc[0][2 * h], old[h][1] + acc[1][2 * h], old[h][2] + acc[2][2 * h],
-                         old[h][3] + acc[3][2 * h]);
-      f[1] = make_float4(old[h][4] + acc[0][2 * h + 1], old[h][5] + acc[1][2 * h + 1], old[h][6] + acc[2][2 * h + 1],
-                         old[h][7] + acc[3][2 * h + 1]);
+        for (int i = 0; i < 4; ++i)
+          if (lo + 8 * i < L)
+            *reinterpret_cast<float2 *>(o + 8 * i) =
+                make_float2(old[h][2 * i] + acc[i][2 * h], old[h][2 * i + 1] + acc[i][2 * h + 1]);
+      } else if (lo < L) {
+        // columns lo + 0 .. 3 are this lane's first column of tiles 0 .. 3, lo + 4 .. 7 its second
+        float4 *f = reinterpret_cast<float4 *>(o);
+        f[0] = make_float4(old[h][0] + acc[0][2 * h], old[h][1] + acc[1][2 * h], old[h][2] + acc[2][2 * h],
+                           old[h][3] + acc[3][2 * h]);
+        f[1] = make_float4(old[h][4] + acc[0][2 * h + 1], old[h][5] + acc[1][2 * h + 1], old[h][6] + acc[2][2 * h + 1],
+                           old[h][7] + acc[3][2 * h + 1]);
+      }
     }
   }
 }
@@ -1066,6 +1090,7 @@ cudaError_t launch_lora_prep(const LoraArgs &a, bool operands, int sms, cudaStre
   const int64_t units = (int64_t)a.T * ((a.K + 511) / 512) + (int64_t)a.N * a.K / 2048 + (int64_t)a.N * a.K / 8192;
   int64_t ctas = operands ? units / 32 + 1 : 0;
   if (ctas > 2 * sms) ctas = 2 * sms;
+  if (a.wexp != nullptr) ctas = (a.N + 31) / 32;
   k_lora_prep<<<(unsigned)(1 + ctas), 1024, smem, s>>>(a, warps);
   return cudaGetLastError();
 }
@@ -1080,13 +1105,18 @@ cudaError_t launch_lora_shrink(const LoraArgs &a, const float *src, int L, const
 }
 
 cudaError_t launch_lora_expand(const LoraArgs &a, const float *v, const void *M, bool l_major, int L, float *dst,
-                               cudaStream_t s) {
-  const dim3 grid((unsigned)lora_tiles(a), (unsigned)((L + 255) / 256));
+                               int sms, cudaStream_t s) {
+  // one wave of two CTAs per SM, if the tiles do not make more of themselves
+  const int tiles = lora_tiles(a), blocks = (L + 255) / 256;
+  int per = (int)((int64_t)tiles * blocks / (2 * sms));
+  per = per < 1 ? 1 : per > blocks ? blocks : per;
+  const int cols = 256 * per;
+  const dim3 grid((unsigned)tiles, (unsigned)((L + cols - 1) / cols));
   if (l_major)
-    return a.bf16 ? launch_pdl(k_lora_expand<true, true>, grid, dim3(256), 0, s, a, v, M, L, dst)
-                  : launch_pdl(k_lora_expand<false, true>, grid, dim3(256), 0, s, a, v, M, L, dst);
-  return a.bf16 ? launch_pdl(k_lora_expand<true, false>, grid, dim3(256), 0, s, a, v, M, L, dst)
-                : launch_pdl(k_lora_expand<false, false>, grid, dim3(256), 0, s, a, v, M, L, dst);
+    return a.bf16 ? launch_pdl(k_lora_expand<true, true>, grid, dim3(256), 0, s, a, v, M, L, dst, cols)
+                  : launch_pdl(k_lora_expand<false, true>, grid, dim3(256), 0, s, a, v, M, L, dst, cols);
+  return a.bf16 ? launch_pdl(k_lora_expand<true, false>, grid, dim3(256), 0, s, a, v, M, L, dst, cols)
+                : launch_pdl(k_lora_expand<false, false>, grid, dim3(256), 0, s, a, v, M, L, dst, cols);
 }
 
 cudaError_t launch_lora_small(const LoraArgs &a, cudaStream_t s) {
@@ -1101,7 +1131,7 @@ cudaError_t launch_lora_large(const LoraArgs &a, int sms, cudaStream_t s) {
   // without the shrink between them the GEMM follows the layout directly, and waits for it
   err = base(a, adapters, s);
   if (err != cudaSuccess || a.n == 0) return err;
-  return launch_lora_expand(a, a.us, a.B, true, a.N, a.out, s);
+  return launch_lora_expand(a, a.us, a.B, true, a.N, a.out, sms, s);
 }
 
 }  // namespace moe

@@ -53,6 +53,15 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// 2^e with e such that |m| 2^e lies in [2^14, 2^15) (1 for 0 and for what is
+// not finite, whose products are not finite at any scale).
+__device__ __forceinline__ float pow2_to_15(float m) {
+  if (!(m > 0.0f) || !(m <= 3.0e38f)) return 1.0f;
+  const int e = (int)(__float_as_uint(m) >> 23) - 127;  // -127 for denormals, which stay small
+  const int k = min(max(14 - e, -126), 126);
+  return __uint_as_float((uint32_t)(k + 127) << 23);
+}
+
 // A value as fp16 hi + lo, 22 significant bits within fp16's range.
 __device__ __forceinline__ void split_f16(float v, __half &hi, __half &lo) {
   hi = __float2half_rn(v);
@@ -196,6 +205,6 @@ cudaError_t launch_lora_shrink(const LoraArgs &a, const float *src, int L, const
                                float *user, int sms, cudaStream_t s);
 // dst[t][l] += sum_j v[p][j] M_a(j, l); M_a(j, l) = A_a[j][l], or B_a[l][j] if `l_major`.
 cudaError_t launch_lora_expand(const LoraArgs &a, const float *v, const void *M, bool l_major, int L, float *dst,
-                               cudaStream_t s);
+                               int sms, cudaStream_t s);
 
 }  // namespace moe

@@ -7,11 +7,11 @@
 //
 // (W^ is frozen; the Q8_0 rounding of x passes gradients unchanged).
 //
-//   k_lora_prep    : tokens by adapter (moe_lora.cu);
+//   k_lora_prep    : tokens by adapter, powers of two of W's rows (moe_lora.cu);
 //   k_lora_shrink  : v, and u where the caller kept none (moe_lora.cu);
 //   k_lora_outer   : dA and dB, a tile of the matrix per CTA, its warps
 //                    splitting the adapter's tokens (tf32 hi + lo, three MMAs);
-//   k_lora_wexp, k_lora_wt, k_lora_gsplit: fp16 hi + lo of W^' and of g;
+//   k_lora_lay     : fp16 hi + lo of W^' and of g;
 //   k_lora_dx      : W^' g on the fifth-generation tensor cores;
 //   k_lora_expand  : adds A_a' v.
 //
@@ -28,15 +28,6 @@
 
 namespace moe {
 namespace {
-
-// 2^e with e such that |m| 2^e lies in [2^14, 2^15) (1 for 0 and for what is
-// not finite, whose products are not finite at any scale).
-__device__ __forceinline__ float pow2_to_15(float m) {
-  if (!(m > 0.0f) || !(m <= 3.0e38f)) return 1.0f;
-  const int e = (int)(__float_as_uint(m) >> 23) - 127;  // -127 for denormals, which stay small
-  const int k = min(max(14 - e, -126), 126);
-  return __uint_as_float((uint32_t)(k + 127) << 23);
-}
 
 // ===========================================================================
 // dA, dB: D[j][l] = sum over the adapter's tokens of left[p][j] right[t][l].
@@ -69,6 +60,7 @@ __global__ void __launch_bounds__(256, 2) k_lora_outer(const LoraArgs a, const f
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int id = blockIdx.y, r = a.r;
   const int l0 = blockIdx.x * kOuterL, lb = l0 + (warp & 1) * 32, j0 = blockIdx.z * kOuterJ, tw = warp >> 1;
+  pdl_wait();
   const int p0 = a.off[id], p1 = a.off[id + 1], steps = (p1 - p0 + kOuterT - 1) / kOuterT;
   const float sc = left_by_token ? a.scale[id] : 1.0f;
   // this thread's copies of a stage: row tid / 8, 16-byte pieces tid % 8 and + 8 of both sides
@@ -185,28 +177,11 @@ __global__ void __launch_bounds__(256, 2) k_lora_outer(const LoraArgs a, const f
 // ===========================================================================
 // operands of the base product
 // ===========================================================================
-// wexp[n] = the power of two of row n of W (from its largest scale), wexp[N + n] its inverse.
-__global__ void __launch_bounds__(256) k_lora_wexp(const LoraArgs a) {
-  const int n = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (n >= a.N) return;
-  const int G = a.K / 64;
-  const __half *sc = reinterpret_cast<const __half *>(a.W + (size_t)a.N * (a.K / 2)) + (size_t)n * G;
-  float m = 0.0f;
-  for (int g = lane; g < G; g += 32) m = fmaxf(m, fabsf(__half2float(sc[g])));
-  m = warp_max(m);
-  if (lane == 0) {
-    const float e = pow2_to_15(8.0f * m);
-    a.wexp[n] = e;
-    // a row of zeros must not set the power of two of g's rows
-    a.wexp[a.N + n] = m == 0.0f ? 0.0f : 1.0f / e;
-  }
-}
-
-// wt [K][2 Np]: per 64 rows of W 64 hi then 64 lo of column k, times wexp[n];
-// a CTA transposes 64 rows by one 64-group.
-__global__ void __launch_bounds__(256) k_lora_wt(const LoraArgs a) {
+// wt [K][2 Np]: per 64 rows of W 64 hi then 64 lo of column k, times wexp[n]; a
+// CTA transposes 64 rows by one 64-group.
+__device__ __forceinline__ void lay_wt(const LoraArgs &a, int n_tile, int g) {
   __shared__ __half hi[64][72], lo[64][72];  // [k][n]
-  const int n0 = blockIdx.x * 64, g = blockIdx.y, G = a.K / 64;
+  const int n0 = n_tile * 64, G = a.K / 64;
   const int tid = threadIdx.x, n = tid & 63, part = tid >> 6;  // 8 packed bytes each
   uint2 w = make_uint2(0x88888888u, 0x88888888u);
   float s = 0.0f;
@@ -235,9 +210,9 @@ __global__ void __launch_bounds__(256) k_lora_wt(const LoraArgs a) {
 
 // gs [T][2 Np]: g's row over wexp, times a power of two of its own; gexp[t] =
 // its inverse.
-__global__ void __launch_bounds__(256) k_lora_gsplit(const LoraArgs a) {
+__device__ __forceinline__ void lay_g(const LoraArgs &a, int t) {
   __shared__ float wm[8];
-  const int t = blockIdx.x, tid = threadIdx.x;
+  const int tid = threadIdx.x;
   const float *g = a.g + (size_t)t * a.N, *inv = a.wexp + a.N;
   const int Np = (a.N + 63) / 64 * 64;
   float m = 0.0f;
@@ -267,6 +242,13 @@ __global__ void __launch_bounds__(256) k_lora_gsplit(const LoraArgs a) {
     *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(h);
     *reinterpret_cast<uint2 *>(o + 64) = *reinterpret_cast<const uint2 *>(l);
   }
+}
+
+// One launch lays out both: the first CTAs tiles of W, the others a row of g each.
+__global__ void __launch_bounds__(256) k_lora_lay(const LoraArgs a, int w_tiles, int n_tiles) {
+  pdl_wait();
+  if ((int)blockIdx.x < w_tiles) lay_wt(a, (int)blockIdx.x % n_tiles, (int)blockIdx.x / n_tiles);
+  else lay_g(a, (int)blockIdx.x - w_tiles);
 }
 
 // ===========================================================================
@@ -324,6 +306,7 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_wait();
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kDxRegsOther));
     if (warp == kDxTmaWarp) {
@@ -443,8 +426,7 @@ cudaError_t outer_rows(const LoraArgs &a, const float *left, int by_token, const
   static int smem_set[64] = {0};
   const cudaError_t err = ensure_smem(k_lora_outer<RM>, kOuterSmem, smem_set);
   if (err != cudaSuccess) return err;
-  k_lora_outer<RM><<<grid, 256, kOuterSmem, s>>>(a, left, by_token, right, L, out, l_major);
-  return cudaGetLastError();
+  return launch_pdl(k_lora_outer<RM>, grid, dim3(256), kOuterSmem, s, a, left, by_token, right, L, out, l_major);
 }
 
 cudaError_t outer(const LoraArgs &a, const float *left, int by_token, const float *right, int L, float *out,
@@ -465,12 +447,11 @@ cudaError_t base_dx(const LoraArgs &a, cudaStream_t s) {
   static std::atomic<int> regs{0};
   if (err == cudaSuccess) err = launch_regs_ok(k_lora_dx, kDxLaunchRegs, regs);
   if (err != cudaSuccess) return err;
-  k_lora_wexp<<<(unsigned)((a.N + 7) / 8), 256, 0, s>>>(a);
-  k_lora_wt<<<dim3((unsigned)(Np / 64), (unsigned)(a.K / 64)), 256, 0, s>>>(a);
-  k_lora_gsplit<<<(unsigned)a.T, 256, 0, s>>>(a);
-  k_lora_dx<<<dim3((unsigned)((a.K + kDxCol - 1) / kDxCol), (unsigned)((a.T + kDxTok - 1) / kDxTok)), kDxThreads,
-              kDxSmem, s>>>(a, gmap, wmap);
-  return cudaGetLastError();
+  const int n_tiles = Np / 64, w_tiles = n_tiles * (a.K / 64);
+  err = launch_pdl(k_lora_lay, dim3((unsigned)(w_tiles + a.T)), dim3(256), 0, s, a, w_tiles, n_tiles);
+  if (err != cudaSuccess) return err;
+  return launch_pdl(k_lora_dx, dim3((unsigned)((a.K + kDxCol - 1) / kDxCol), (unsigned)((a.T + kDxTok - 1) / kDxTok)),
+                    dim3(kDxThreads), kDxSmem, s, a, gmap, wmap);
 }
 
 }  // namespace
@@ -488,7 +469,7 @@ cudaError_t launch_lora_bwd(const LoraArgs &a, int sms, cudaStream_t s) {
   if (err != cudaSuccess || a.dx == nullptr || a.T == 0) return err;
   err = base_dx(a, s);
   if (err != cudaSuccess || a.n == 0) return err;
-  return launch_lora_expand(a, a.v, a.A, false, a.K, a.dx, s);
+  return launch_lora_expand(a, a.v, a.A, false, a.K, a.dx, sms, s);
 }
 
 }  // namespace moe
