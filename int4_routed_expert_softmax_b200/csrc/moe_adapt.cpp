@@ -32,7 +32,7 @@ int check_lora(const moe_lora_dims *p, int32_t T) {
 
 struct LoraLayout {
   size_t status, perm, off, tile, us;     // both calls
-  size_t xq, xs, upart;                   // forward, small batches
+  size_t xq, xs;                          // forward, small batches
   size_t xh, wh, xd, ws;                  // forward, larger ones
   size_t v, wt, gs, gexp, wexp;           // backward
   size_t total;
@@ -62,7 +62,6 @@ LoraLayout lora_layout(const moe_lora_dims &p, int T, bool backward) {
   } else {
     L.xq = seg(kLoraSmallT * K);
     L.xs = seg((size_t)kLoraSmallT / 2 * (K / 64) * kXs * 4);
-    L.upart = seg((K + kLoraSlice - 1) / kLoraSlice * (size_t)kLoraSmallT * r * 4);
     if (T > kLoraSmallT) {
       L.xh = seg(Tp * K * 4);
       L.wh = seg(N * K * 2);
@@ -167,7 +166,6 @@ int moe_lora_forward(const moe_lora_dims *dims, int32_t T, const float *x, const
   a.u = u_opt;
   a.xq = at<int8_t>(ws, L.xq);
   a.xs = at<float>(ws, L.xs);
-  a.upart = at<float>(ws, L.upart);
   a.xh = at<__half>(ws, L.xh);
   a.wh = at<__half>(ws, L.wh);
   a.xd = at<float>(ws, L.xd);

@@ -324,8 +324,7 @@ cudaError_t launch_balance_fwd(const BalanceArgs &a, int grid, cudaStream_t s);
 cudaError_t launch_balance_bwd(const BalanceArgs &a, int sms, cudaStream_t s);
 
 // int4 projection with low-rank adapters (moe_lora.cu, moe_lora_bwd.cu).
-constexpr int kLoraSmallT = 16;      // the largest batch the small kernels take (their CTAs hold all its codes)
-constexpr int kLoraSlice = 512;      // inputs per CTA of their first kernel
+constexpr int kLoraSmallT = 64;      // the largest batch the small kernels take (moe_lora.cu)
 constexpr int kLoraMaxRank = 128;
 constexpr int kLoraMaxAdapters = 4096;
 constexpr int kLoraTile = 128;       // rows of the workspace are padded to this many tokens
@@ -348,8 +347,7 @@ struct LoraArgs {
   __half *xh, *wh;          // larger ones: [T][2K] x^ over its group's scale, hi and lo, and [N][K] W's integers
   float *xd, *ws;           // [K / 64][Tp] scales of x's groups, [K / 64][Nt] of W's
   int Nt;                   // row length of ws: N in whole tiles
-  float *upart;             // [slices][T][r] partial A x (token order)
-  float *us;                // [Tp][r] scale * A x by sorted position
+  float *us;                // [Tp][r] scale * A x by sorted position (small batches: by token)
   int32_t *perm, *off, *tile;  // sorted order: token of each position, first position and tile per adapter
   // backward
   const float *g;           // [T][N]

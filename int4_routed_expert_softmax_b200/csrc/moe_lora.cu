@@ -15,7 +15,7 @@
 // tokens by 2048 x 6144).
 //
 // Small batches (at most kLoraSmallT tokens): two launches in token order.
-//   k_lora_in    : Q8_0 of x, and partial sums of A x per slice of the inputs;
+//   k_lora_in    : Q8_0 of x, and scale A x, a cluster per token;
 //   k_lora_proj  : 16 rows of W per CTA, its eight warps splitting the inputs;
 //                  the weights are loaded into registers before the wait for
 //                  k_lora_in, so that the two overlap.
@@ -57,54 +57,67 @@ __device__ __forceinline__ int4 quant4(const float4 v, float &d) {
 // ===========================================================================
 // small batches
 // ===========================================================================
+// A cluster takes a token, each of its CTAs a share of the inputs (at most
+// kInShare, four a thread): their Q8_0 codes, and their part of A x, which the
+// first CTA sums up in a fixed order.
+constexpr int kInShare = 1024;
+
 template <bool BF16>
-__global__ void __launch_bounds__(128) k_lora_in(const LoraArgs a) {
-  __shared__ float xsm[kLoraSlice];
+__global__ void __launch_bounds__(256) k_lora_in(const LoraArgs a) {
+  __shared__ __align__(16) float xsm[kInShare];
+  __shared__ float part[kLoraMaxRank];
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int t = blockIdx.y, k0 = blockIdx.x * kLoraSlice;
-  const int G = a.K / 64, r = a.r;
+  const int t = blockIdx.y, G = a.K / 64, r = a.r;
+  const int shares = (int)gridDim.x, share = (int)blockIdx.x;
+  const int k0 = (int)((int64_t)G * share / shares) * 64, k1 = (int)((int64_t)G * (share + 1) / shares) * 64;
   pdl_launch_dependents();
-  if (blockIdx.x == 0 && t == 0 && tid < 4) a.status[tid] = 0;
+  if (share == 0 && t == 0 && tid < 4) a.status[tid] = 0;
   const int k = k0 + 4 * tid;
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (k < a.K) v = *reinterpret_cast<const float4 *>(a.x + (size_t)t * a.K + k);
+  if (k < k1) v = *reinterpret_cast<const float4 *>(a.x + (size_t)t * a.K + k);
   const int id = adapter_of(a, t);
   float d;
   const int4 q = quant4(v, d);
   int sum = q.x + q.y + q.z + q.w;
 #pragma unroll
   for (int off = 4; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (k < a.K) {
+  if (k < k1) {
     *reinterpret_cast<char4 *>(a.xq + (size_t)t * a.K + k) =
         make_char4((signed char)q.x, (signed char)q.y, (signed char)q.z, (signed char)q.w);
     if ((tid & 7) == 0) store_xs(a.xs, t, G, k, d, kMagicBits - 8 * sum);
   }
-  if (id == a.n) return;
+  if (id == a.n) {  // one decision for the cluster: all of it has this token
+    if (share == 0)
+      for (int j = tid; j < r; j += 256) {
+        a.us[(size_t)t * r + j] = 0.0f;
+        if (a.u != nullptr) a.u[(size_t)t * r + j] = 0.0f;
+      }
+    return;
+  }
   *reinterpret_cast<float4 *>(xsm + 4 * tid) = v;
   __syncthreads();
-  // rows j = warp, warp + 4, .., four of them loaded at once: lane = 16 of the
-  // slice's inputs (8 + 8)
+  // rows j = warp, warp + 8, .., four of them at once: lane = 8 of 256 inputs
   const uint16_t *A = static_cast<const uint16_t *>(a.A) + (size_t)id * r * a.K + k0;
-  float *dst = a.upart + ((size_t)blockIdx.x * a.T + t) * r;
-  for (int j0 = warp; j0 < r; j0 += 16) {
-    uint4 w[4][2];
-#pragma unroll
-    for (int m = 0; m < 4; ++m)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = h * 256 + lane * 8, j = j0 + 4 * m;
-        w[m][h] = j < r && k0 + i < a.K ? __ldg(reinterpret_cast<const uint4 *>(A + (size_t)j * a.K + i))
-                                        : make_uint4(0u, 0u, 0u, 0u);
-      }
+  for (int j0 = warp; j0 < r; j0 += 32) {
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+    for (int i0 = 0; i0 < k1 - k0; i0 += 256) {
+      const int i = i0 + lane * 8;
+      uint4 w[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 *xp = reinterpret_cast<const float4 *>(xsm + h * 256 + lane * 8);
+      for (int m = 0; m < 4; ++m) {
+        const int j = j0 + 8 * m;
+        w[m] = j < r && k0 + i < k1 ? __ldg(reinterpret_cast<const uint4 *>(A + (size_t)j * a.K + i))
+                                    : make_uint4(0u, 0u, 0u, 0u);
+      }
+      const float4 *xp = reinterpret_cast<const float4 *>(xsm + i);
       const float4 x0 = xp[0], x1 = xp[1];
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const float2 a0 = half2_values<BF16>(w[m][h].x), a1 = half2_values<BF16>(w[m][h].y);
-        const float2 a2 = half2_values<BF16>(w[m][h].z), a3 = half2_values<BF16>(w[m][h].w);
+        const float2 a0 = half2_values<BF16>(w[m].x), a1 = half2_values<BF16>(w[m].y);
+        const float2 a2 = half2_values<BF16>(w[m].z), a3 = half2_values<BF16>(w[m].w);
         s[m] = ffma(a0.x, x0.x, s[m]);
         s[m] = ffma(a0.y, x0.y, s[m]);
         s[m] = ffma(a1.x, x0.z, s[m]);
@@ -119,8 +132,17 @@ __global__ void __launch_bounds__(128) k_lora_in(const LoraArgs a) {
     for (int off = 16; off >= 1; off >>= 1)
 #pragma unroll
       for (int m = 0; m < 4; ++m) s[m] += __shfl_xor_sync(0xffffffffu, s[m], off);
-    if (lane < 4 && j0 + 4 * lane < r) dst[j0 + 4 * lane] = lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3];
+    if (lane < 4 && j0 + 8 * lane < r) part[j0 + 8 * lane] = lane == 0 ? s[0] : lane == 1 ? s[1] : lane == 2 ? s[2] : s[3];
   }
+  cluster.sync();
+  if (share == 0)
+    for (int j = tid; j < r; j += 256) {
+      float u = 0.0f;
+      for (int c = 0; c < shares; ++c) u += cluster.map_shared_rank(part, c)[j];
+      a.us[(size_t)t * r + j] = a.scale[id] * u;
+      if (a.u != nullptr) a.u[(size_t)t * r + j] = u;
+    }
+  cluster.sync();  // the parts stay until they have been read
 }
 
 constexpr int kProjPre = 12;  // groups a warp holds in registers (12 * 8 warps * 64 = 6144 inputs)
@@ -150,6 +172,8 @@ __device__ __forceinline__ void group_mma(f32x2 (&acc)[2], const NibblePair &w, 
   acc[1] = fma2(th, s1, acc[1]);
 }
 
+constexpr int kProjTok = 16;  // tokens per CTA at most
+
 // Shared memory of k_lora_proj: the codes and the scales of all tokens as rows
 // padded by 32 bytes, so that the rows that half a warp reads start on
 // different banks; the row sums of the eight warps; scale A x; W's scales.
@@ -174,7 +198,8 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
   extern __shared__ __align__(128) unsigned char psm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, q4 = lane & 3;
-  const int G = a.K / 64, N = a.N, r = a.r, T = a.T;
+  const int G = a.K / 64, N = a.N, r = a.r;
+  const int tb = blockIdx.y * kProjTok, T = min(a.T - tb, kProjTok);  // this CTA's tokens: tb .. tb + T
   const ProjLayout L = proj_layout(a.K, r, NT);
   uint64_t *landed = reinterpret_cast<uint64_t *>(psm);        // the codes and every scale
   float *red = reinterpret_cast<float *>(psm + L.red);         // [8][16][NT * 8]
@@ -206,7 +231,7 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
   load_w(0);
   // this thread's output (the first of them) and its row of B, brought near
   const int row = tid & 15, t1 = tid >> 4;
-  const int id1 = t1 < T ? adapter_of(a, t1) : a.n;
+  const int id1 = t1 < T ? adapter_of(a, tb + t1) : a.n;
   const uint16_t *Bn = static_cast<const uint16_t *>(a.B);
   if (id1 < a.n && n0 + row < N)
     asm volatile("prefetch.global.L1 [%0];" ::"l"(Bn + ((size_t)id1 * N + n0 + row) * r) : "memory");
@@ -214,22 +239,11 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
   if (tid == 0) {
     const int pairs = (T + 1) / 2;
     mbar_arrive_expect_tx(landed, (uint32_t)(T * a.K + pairs * G * kXs * 4));
-    for (int t = 0; t < T; ++t) bulk_g2s(psm + 16 + t * L.crow, a.xq + (size_t)t * a.K, (uint32_t)a.K, landed);
+    for (int t = 0; t < T; ++t) bulk_g2s(psm + 16 + t * L.crow, a.xq + (size_t)(tb + t) * a.K, (uint32_t)a.K, landed);
     for (int i = 0; i < pairs; ++i)
-      bulk_g2s(psm + L.xs + i * L.xrow, a.xs + (size_t)i * G * kXs, (uint32_t)(G * kXs * 4), landed);
+      bulk_g2s(psm + L.xs + i * L.xrow, a.xs + (size_t)(tb / 2 + i) * G * kXs, (uint32_t)(G * kXs * 4), landed);
   }
-  // A x of the tokens, the slices in order
-  const int slices = (a.K + kLoraSlice - 1) / kLoraSlice;
-  for (int i = tid; i < T * r; i += 256) {
-    const int t = i / r, id = adapter_of(a, t);
-    float u = 0.0f;
-    if (id < a.n) {
-#pragma unroll 4
-      for (int s = 0; s < slices; ++s) u += a.upart[(size_t)s * T * r + i];
-    }
-    if (blockIdx.x == 0 && a.u != nullptr) a.u[i] = u;
-    us[i] = id < a.n ? a.scale[id] * u : 0.0f;
-  }
+  for (int i = tid; i < T * r; i += 256) us[i] = a.us[(size_t)tb * r + i];
   __syncthreads();  // the barrier is initialised for every thread
   bool ok = mbar_wait(landed, 0, a.status, kDetLoraProj, a.wait_limit);
   f32x2 acc[NT][2];
@@ -271,12 +285,12 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
     float o = 0.0f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) o += red[(w * 16 + row) * (NT * 8) + t];
-    const int id = adapter_of(a, t);
+    const int id = adapter_of(a, tb + t);
     if (id < a.n) {
       const uint4 *B = reinterpret_cast<const uint4 *>(Bn + ((size_t)id * N + n0 + row) * r);
       const float *ut = us + t * r;
       float l = 0.0f;
-#pragma unroll 2
+#pragma unroll 4
       for (int j = 0; j < r / 8; ++j) {
         const uint4 w = __ldg(B + j);
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
@@ -289,7 +303,7 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
       }
       o += l;
     }
-    a.out[(size_t)t * N + n0 + row] = o;
+    a.out[(size_t)(tb + t) * N + n0 + row] = o;
   }
 }
 
@@ -1007,13 +1021,25 @@ cudaError_t proj(const LoraArgs &a, cudaStream_t s) {
   static int smem_set[64] = {0};
   cudaError_t err = ensure_smem(k_lora_proj<NT, BF16>, smem, smem_set);
   if (err != cudaSuccess) return err;
-  return launch_pdl(k_lora_proj<NT, BF16>, dim3((unsigned)((a.N + 15) / 16)), dim3(256), smem, s, a);
+  return launch_pdl(k_lora_proj<NT, BF16>, dim3((unsigned)((a.N + 15) / 16), (unsigned)((a.T + kProjTok - 1) / kProjTok)),
+                    dim3(256), smem, s, a);
 }
 
 template <bool BF16>
 cudaError_t small(const LoraArgs &a, cudaStream_t s) {
-  k_lora_in<BF16><<<dim3((unsigned)((a.K + kLoraSlice - 1) / kLoraSlice), (unsigned)a.T), 128, 0, s>>>(a);
-  cudaError_t err = cudaGetLastError();
+  // as many CTAs per token as a portable cluster has, 256 inputs each at least
+  const int G = a.K / 64, shares = G >= 32 ? 8 : G >= 4 ? G / 4 : 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)shares, (unsigned)a.T);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)shares;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  cudaError_t err = cudaLaunchKernelEx(&cfg, k_lora_in<BF16>, a);
   if (err != cudaSuccess) return err;
   if (a.T <= 8) return proj<1, BF16>(a, s);
   return proj<2, BF16>(a, s);
