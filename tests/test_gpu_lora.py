@@ -57,8 +57,9 @@ SHAPES = [
     # T, K, N, n, r: the kernels of small batches
     (1, 64, 8, 1, 8), (1, 6144, 64, 3, 16), (2, 128, 24, 2, 8), (7, 192, 40, 4, 24), (8, 2048, 136, 40, 16),
     (9, 576, 72, 3, 128), (16, 2048, 256, 16, 16), (17, 1088, 16, 5, 64), (31, 8192, 32, 2, 40), (32, 512, 200, 33, 32),
+    (33, 64, 8, 1, 8), (48, 576, 72, 3, 128), (63, 6144, 40, 20, 64), (64, 64, 2048, 1, 8),
     # tokens sorted by adapter
-    (33, 64, 8, 1, 8), (64, 192, 72, 3, 24), (65, 1088, 136, 70, 16), (127, 512, 1000, 4, 128), (200, 2048, 264, 24, 32),
+    (65, 64, 8, 1, 8), (66, 6144, 40, 20, 8), (128, 2048, 256, 9, 8), (385, 8192, 1000, 3, 32), (64, 192, 72, 3, 24), (65, 1088, 136, 70, 16), (127, 512, 1000, 4, 128), (200, 2048, 264, 24, 32),
     (300, 8192, 64, 2, 40), (513, 320, 2048, 8, 64), (2100, 128, 1288, 6, 16),
 ]
 
@@ -302,3 +303,39 @@ def test_workspace_of_a_larger_batch_serves_smaller_ones():
         m.moe_lora_forward(p, *case[:6], out, dirty(ws))
         ref, _, bo, _ = ad.lora_forward(case[1], case[0], *case[2:6], 72, 256)
         close(out, ref, bo, "out")
+
+
+@pytest.mark.parametrize("T,what", [(1, "fwd"), (16, "fwd"), (40, "fwd"), (200, "fwd"), (1500, "fwd"), (100, "bwd"), (700, "bwd")])
+def test_waits_that_run_out(T, what):
+    """A short wait limit makes the kernels' waits for data give up: the status word says so, and the device,
+    the workspace and later calls stay usable."""
+    m = moe()
+    K, N, n, r = 1024, 512, 3, 16
+    case = inputs(T, K, N, n, r, torch.bfloat16)
+    x, W, A, B, scale, adapter, g = case
+    p = m.lora(K, N, n, r)
+    ws = m.alloc_lora_workspace(p, T, backward=True)
+
+    def call():
+        if what == "fwd":
+            o = torch.zeros(T, N, device="cuda")
+            m.moe_lora_forward(p, x, W, A, B, scale, adapter, o, ws)
+        else:
+            o = torch.zeros(T, K, device="cuda")
+            m.moe_lora_backward(p, g, x, W, A, B, scale, adapter, ws, dx=o)
+        torch.cuda.synchronize()
+        return o, int(ws[:4].view(torch.int32))
+
+    want, status = call()
+    assert status == 0
+    old = m.moe_set_wait_limit(1)
+    try:
+        got, status = call()
+    finally:
+        m.moe_set_wait_limit(old)
+    if T <= 64 and what == "fwd" and status == 0:  # one wait: its copies may have landed before the first look
+        assert torch.equal(got, want)
+    else:
+        assert status == -7
+    got, status = call()
+    assert status == 0 and torch.equal(got, want)
