@@ -1045,33 +1045,6 @@ cudaError_t small(const LoraArgs &a, cudaStream_t s) {
   return proj<2, BF16>(a, s);
 }
 
-// How many clusters of `shares` CTAs of k_lora_base fit on the device at once
-// (its GPCs hold whole clusters only); asked once per device and size.
-int base_clusters(int shares) {
-  static std::atomic<int> known[64][9];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  int n = known[dev][shares].load(std::memory_order_relaxed);
-  if (n == 0) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(1, 1, (unsigned)shares);
-    cfg.blockDim = dim3(kBaseThreads);
-    cfg.dynamicSmemBytes = kBaseSmem;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = at.val.clusterDim.y = 1;
-    at.val.clusterDim.z = (unsigned)shares;
-    cfg.attrs = &at;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, k_lora_base, &cfg) != cudaSuccess || n < 1) {
-      cudaGetLastError();
-      n = -1;
-    }
-    known[dev][shares].store(n, std::memory_order_relaxed);
-  }
-  return n;
-}
-
 cudaError_t base(const LoraArgs &a, bool pdl, cudaStream_t s) {
   static int smem_set[64] = {0};
   cudaError_t err = ensure_smem(k_lora_base, kBaseSmem, smem_set);
@@ -1085,9 +1058,10 @@ cudaError_t base(const LoraArgs &a, bool pdl, cudaStream_t s) {
   // groups.  (Narrower tiles instead were no way out: a group cost a CTA nearly
   // the same for 64 columns as for 256.)
   const int64_t tiles = (int64_t)((a.T + 127) / 128) * ((a.N + kBaseN - 1) / kBaseN);
+  static std::atomic<int> known[64][9];
   int shares = 1;
   for (int c = 2; c <= 8 && a.K / 64 / c >= 4; ++c)
-    if (tiles <= base_clusters(c)) shares = c;
+    if (tiles <= max_clusters(k_lora_base, kBaseThreads, kBaseSmem, c, known)) shares = c;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((a.N + kBaseN - 1) / kBaseN), (unsigned)((a.T + 127) / 128), (unsigned)shares);
   cfg.blockDim = dim3(kBaseThreads);

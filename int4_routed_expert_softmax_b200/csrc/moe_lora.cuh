@@ -177,6 +177,55 @@ inline cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, dim3 block, size_
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The same in clusters.
+template <typename... P, typename... A>
+inline cudaError_t launch_cluster_pdl(void (*kernel)(P...), dim3 grid, dim3 block, dim3 cluster, size_t smem,
+                                      cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = cluster.x;
+  at[0].val.clusterDim.y = cluster.y;
+  at[0].val.clusterDim.z = cluster.z;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// How many clusters of 1 x 1 x `size` CTAs of a kernel fit on the device at once
+// (its GPCs hold whole clusters only).  Asked once per device and size; `known`:
+// the kernel's own record.  The kernel's shared-memory limit is set before.
+template <typename K>
+inline int max_clusters(K kernel, int threads, size_t smem, int size, std::atomic<int> (&known)[64][9]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][size].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1, 1, (unsigned)size);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = (unsigned)size;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = -1;
+    }
+    known[dev][size].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 // A kernel that splits its registers with setmaxnreg counts on those it was
 // launched with: a build that gave it others would leave setmaxnreg.inc
 // waiting, and is refused.  `known`: the kernel's own record of its count.

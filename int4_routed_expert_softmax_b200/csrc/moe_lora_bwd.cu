@@ -23,6 +23,8 @@
 // row of g by one of its own, undone in the epilogue.  An int4 weight times
 // its fp16 scale has at most 15 significant bits, so W^' is exact in hi + lo as
 // long as a group's scale is within 2^-15 of its row's largest.
+#include <cooperative_groups.h>
+
 #include "moe_lora.cuh"
 #include "moe_umma.cuh"
 
@@ -252,20 +254,27 @@ __global__ void __launch_bounds__(256) k_lora_lay(const LoraArgs a, int w_tiles,
 }
 
 // ===========================================================================
-// dx = g W^: tiles of 128 tokens by 256 inputs, one CTA each.  Warp 8 loads
-// (TMA, two stages of 64 of the N reduction: 128 + 256 rows of hi and lo),
-// warp 9 issues the MMAs, warps 0-7 hold the sums in registers: a warp has one
-// quarter of the tokens (its TMEM lanes) by half of the inputs.  They add the
-// accumulator every kDxFlush stages, two accumulators taking turns, because
-// the tensor cores truncate (one accumulator over N = 6144 was off by 2.2e-5;
-// 24 MMAs lose 4e-7).  Every wait is bounded.
+// dx = g W^: tiles of 128 tokens by COL inputs.  Warp 8 loads (TMA, two stages
+// of 64 of the N reduction: 128 + COL rows of hi and lo), warp 9 issues the
+// MMAs, warps 0-7 hold the sums in registers: a warp has one quarter of the
+// tokens (its TMEM lanes) by half of the inputs.  They add the accumulator every
+// kDxFlush stages, two accumulators taking turns, because the tensor cores
+// truncate (one accumulator over N = 6144 was off by 2.2e-5; 24 MMAs lose 4e-7).
+// With few tiles a cluster of CTAs splits N; the sums leave through shared
+// memory, where each CTA of the cluster joins its share of the columns in a
+// fixed order.  Every wait is bounded.
 // ===========================================================================
-constexpr int kDxTok = 128, kDxCol = 256;
+constexpr int kDxTok = 128;
 constexpr int kDxStages = 2;
 constexpr int kDxFlush = 2;
-constexpr uint32_t kDxA = kDxTok * 128, kDxB = kDxCol * 128;      // one of hi, lo
-constexpr uint32_t kDxStage = 2 * (kDxA + kDxB);
-constexpr size_t kDxSmem = 1024 + (size_t)kDxStages * kDxStage + 1024;  // barriers, stages, alignment
+constexpr uint32_t kDxA = kDxTok * 128;  // one of hi, lo
+template <int COL>
+struct DxCfg {
+  static constexpr uint32_t B = COL * 128, STAGE = 2 * (kDxA + B);
+  static constexpr size_t SMEM = 1024 + (size_t)kDxStages * STAGE + 1024;  // barriers, stages, alignment
+  static_assert((size_t)kDxTok * (COL + 4) * 4 <= (size_t)kDxStages * STAGE, "the sums fit the stages");
+};
+constexpr uint32_t kDxAcc = 256;  // columns of tensor memory per accumulator
 // Launched at 168 registers a thread; the two epilogue warpgroups take 216, the
 // third gives its own down to 72: 2 * 128 * 216 + 128 * 72 = 384 * 168.
 constexpr int kDxThreads = 384, kDxLaunchRegs = 168, kDxRegs = 216, kDxRegsOther = 72;
@@ -273,18 +282,23 @@ static_assert(2 * 128 * kDxRegs + 128 * kDxRegsOther <= kDxThreads * kDxLaunchRe
               "register split exceeds the launch's registers");
 constexpr int kDxTmaWarp = 8, kDxMmaWarp = 9;
 
+template <int COL>
 __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, const __grid_constant__ CUtensorMap gmap,
                                                            const __grid_constant__ CUtensorMap wmap) {
   extern __shared__ unsigned char dsm_raw[];
   unsigned char *dsm = dsm_raw + (1024 - (smem_u32(dsm_raw) & 1023)) % 1024;
+  namespace cg = cooperative_groups;
+  using Cfg = DxCfg<COL>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t *full = reinterpret_cast<uint64_t *>(dsm), *empty = full + kDxStages;
   uint64_t *accfull = empty + kDxStages, *accfree = accfull + 2, *done = accfree + 2;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   unsigned char *buf = dsm + 1024;
-  const int k0 = blockIdx.x * kDxCol, t0 = blockIdx.y * kDxTok;
-  const int S = (a.N + 63) / 64, C = (S + kDxFlush - 1) / kDxFlush;
+  const int k0 = blockIdx.x * COL, t0 = blockIdx.y * kDxTok;
+  const int shares = (int)gridDim.z, share = (int)blockIdx.z, all = (a.N + 63) / 64;
+  const int s0 = (int)((int64_t)all * share / shares), S = (int)((int64_t)all * (share + 1) / shares) - s0;
+  const int C = (S + kDxFlush - 1) / kDxFlush;
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     for (int s = 0; s < kDxStages; ++s) {
@@ -299,7 +313,7 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
     fence_barrier_init();
   }
   if (warp == kDxMmaWarp) {
-    tmem_alloc(tmem_slot, 2 * kDxCol);
+    tmem_alloc(tmem_slot, 2 * kDxAcc);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -313,19 +327,18 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
       int issued = 0;
       for (int j = 0; j < S; ++j) {
         const int s = j % kDxStages;
-        if ((j >= kDxStages &&
-             !warp_wait(empty + s, (uint32_t)(j / kDxStages - 1) & 1u, a.status, kDetLoraEmpty, a.wait_limit)) ||
-            __any_sync(0xffffffffu, *abort_flag != 0)) {
+        if (j >= kDxStages &&
+            !warp_wait(empty + s, (uint32_t)(j / kDxStages - 1) & 1u, a.status, kDetLoraEmpty, a.wait_limit)) {
           *abort_flag = 1;
           break;
         }
         if (elect_one()) {
-          unsigned char *b = buf + s * kDxStage;
-          mbar_arrive_expect_tx(full + s, kDxStage);
-          tma_load_2d(b, &gmap, j * 128, t0, full + s);
-          tma_load_2d(b + kDxA, &gmap, j * 128 + 64, t0, full + s);
-          tma_load_2d(b + 2 * kDxA, &wmap, j * 128, k0, full + s);
-          tma_load_2d(b + 2 * kDxA + kDxB, &wmap, j * 128 + 64, k0, full + s);
+          unsigned char *b = buf + s * Cfg::STAGE;
+          mbar_arrive_expect_tx(full + s, Cfg::STAGE);
+          tma_load_2d(b, &gmap, (s0 + j) * 128, t0, full + s);
+          tma_load_2d(b + kDxA, &gmap, (s0 + j) * 128 + 64, t0, full + s);
+          tma_load_2d(b + 2 * kDxA, &wmap, (s0 + j) * 128, k0, full + s);
+          tma_load_2d(b + 2 * kDxA + Cfg::B, &wmap, (s0 + j) * 128 + 64, k0, full + s);
         }
         __syncwarp();
         issued = j + 1;
@@ -334,26 +347,25 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
         mbar_drain(full + j % kDxStages, (uint32_t)(j / kDxStages) & 1u, a.status, kDetLoraDrain);
     }
     if (warp == kDxMmaWarp) {
-      const uint32_t idesc = pf_idesc(kDxCol);
+      const uint32_t idesc = pf_idesc(COL);
       const uint64_t ad0 = umma_desc_sw128(smem_u32(buf));
       for (int j = 0; j < S; ++j) {
         const int s = j % kDxStages, c = j / kDxFlush;
         const bool first = j % kDxFlush == 0;
         if (!warp_wait(full + s, (uint32_t)(j / kDxStages) & 1u, a.status, kDetLoraFull, a.wait_limit) ||
             (first && c >= 2 &&
-             !warp_wait(accfree + (c & 1), (uint32_t)(c / 2 - 1) & 1u, a.status, kDetLoraFree, a.wait_limit)) ||
-            __any_sync(0xffffffffu, *abort_flag != 0)) {
+             !warp_wait(accfree + (c & 1), (uint32_t)(c / 2 - 1) & 1u, a.status, kDetLoraFree, a.wait_limit))) {
           *abort_flag = 1;
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)((c & 1) * kDxCol);
-        const uint64_t ad = ad0 + (uint64_t)((s * kDxStage) >> 4), bd = ad + (uint64_t)((2 * kDxA) >> 4);
+        const uint32_t d = tmem + (uint32_t)(c & 1) * kDxAcc;
+        const uint64_t ad = ad0 + (uint64_t)((s * Cfg::STAGE) >> 4), bd = ad + (uint64_t)((2 * kDxA) >> 4);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint64_t o = (uint64_t)((k * 32) >> 4);
-            umma_f16(d, ad + o, bd + o + (kDxB >> 4), idesc, (uint32_t)(!first || k > 0));
+            umma_f16(d, ad + o, bd + o + (Cfg::B >> 4), idesc, (uint32_t)(!first || k > 0));
             umma_f16(d, ad + o + (kDxA >> 4), bd + o, idesc, 1u);
             umma_f16(d, ad + o, bd + o, idesc, 1u);
           }
@@ -369,27 +381,28 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDxRegs));
+    constexpr int HN = COL / 2;
     const int q = warp & 3, half = warp >> 2;  // TMEM lane quarter, half of the inputs
-    const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * (kDxCol / 2));
-    f32x2 acc[kDxCol / 4];
+    const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * HN);
+    f32x2 acc[HN / 2];
 #pragma unroll
-    for (int i = 0; i < kDxCol / 4; ++i) acc[i] = 0ull;
+    for (int i = 0; i < HN / 2; ++i) acc[i] = 0ull;
     for (int c = 0; c < C; ++c) {
       const bool got = mbar_wait(accfull + (c & 1), (uint32_t)(c / 2) & 1u, a.status, kDetLoraAcc, a.wait_limit);
-      if (!__all_sync(0xffffffffu, got && *abort_flag == 0)) {
+      if (!__all_sync(0xffffffffu, got)) {
         *abort_flag = 1;
         break;
       }
       tc_fence_after();
-      const uint32_t ta = at + (uint32_t)((c & 1) * kDxCol);
+      const uint32_t ta = at + (uint32_t)(c & 1) * kDxAcc;
       // 16 columns at a time, the next ones on their way out of tensor memory meanwhile
       uint32_t v[2][16];
       tmem_ld16(ta, v[0]);
 #pragma unroll
-      for (int i = 0; i < kDxCol / 2; i += 16) {
+      for (int i = 0; i < HN; i += 16) {
         const int b = (i >> 4) & 1;
         tmem_ld_wait();
-        if (i + 16 < kDxCol / 2) {
+        if (i + 16 < HN) {
           tmem_ld16(ta + (uint32_t)(i + 16), v[b ^ 1]);
         } else {
           tc_fence_before();
@@ -400,23 +413,42 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
         for (int x = 0; x < 16; x += 2) acc[(i + x) / 2] = add2(acc[(i + x) / 2], pack2i(v[b][x], v[b][x + 1]));
       }
     }
-    const int t = t0 + q * 32 + lane, kc = k0 + half * (kDxCol / 2);
-    if (*abort_flag == 0 && t < a.T) {
-      const float f = a.gexp[t];
-      const f32x2 f2 = pack2(f, f);
-      float *row = a.dx + (size_t)t * a.K + kc;
+    // the sums to shared memory, over the stages: their last copy and MMA are
+    // complete once all eight warps are here (rows of COL + 4 words spread the
+    // lanes' 16-byte accesses over the banks)
+    named_sync(1, 256);
+    float *mine = reinterpret_cast<float *>(buf) + (q * 32 + lane) * (COL + 4) + half * HN;
 #pragma unroll
-      for (int i = 0; i < kDxCol / 2; i += 4)
-        if (kc + i < a.K)
-          *reinterpret_cast<ulonglong2 *>(row + i) = make_ulonglong2(mul2(f2, acc[i / 2]), mul2(f2, acc[i / 2 + 1]));
-    }
+    for (int i = 0; i < HN; i += 4)
+      *reinterpret_cast<ulonglong2 *>(mine + i) = make_ulonglong2(acc[i / 2], acc[i / 2 + 1]);
   }
+  const bool ok = *abort_flag == 0;
+  cg::cluster_group cluster = cg::this_cluster();
   tc_fence_before();
-  __syncthreads();
+  if (shares > 1) cluster.sync();
+  else __syncthreads();
   if (warp == kDxMmaWarp) {
     tc_fence_after();
-    tmem_dealloc(tmem, 2 * kDxCol);
+    tmem_dealloc(tmem, 2 * kDxAcc);
   }
+  if (ok) {
+    // this CTA's share of the columns, summed over the cluster
+    const int w4 = (COL / 4 + shares - 1) / shares, c0 = share * w4;
+    const int w = min(w4, COL / 4 - c0);
+    for (int i = threadIdx.x; i < kDxTok * w; i += kDxThreads) {
+      const int row = i / w, c = (c0 + i - row * w) * 4;
+      if (t0 + row >= a.T || k0 + c >= a.K) continue;
+      float *p = reinterpret_cast<float *>(buf) + row * (COL + 4) + c;
+      float4 v = *reinterpret_cast<const float4 *>(shares > 1 ? cluster.map_shared_rank(p, 0) : p);
+      for (int r = 1; r < shares; ++r) {
+        const float4 x = *reinterpret_cast<const float4 *>(cluster.map_shared_rank(p, r));
+        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+      }
+      const float f = a.gexp[t0 + row];
+      *reinterpret_cast<float4 *>(a.dx + (size_t)(t0 + row) * a.K + k0 + c) = make_float4(f * v.x, f * v.y, f * v.z, f * v.w);
+    }
+  }
+  if (shares > 1) cluster.sync();  // the sums stay until they have been read
 }
 
 template <int RM>
@@ -436,22 +468,46 @@ cudaError_t outer(const LoraArgs &a, const float *left, int by_token, const floa
   return outer_rows<4>(a, left, by_token, right, L, out, l_major, s);
 }
 
-cudaError_t base_dx(const LoraArgs &a, cudaStream_t s) {
+template <int COL>
+cudaError_t dx_ready() {
+  static int smem_set[64] = {0};
+  cudaError_t err = ensure_smem(k_lora_dx<COL>, DxCfg<COL>::SMEM, smem_set);
+  static std::atomic<int> regs{0};
+  if (err == cudaSuccess) err = launch_regs_ok(k_lora_dx<COL>, kDxLaunchRegs, regs);
+  return err;
+}
+
+template <int COL>
+cudaError_t dx_launch(const LoraArgs &a, int shares, cudaStream_t s) {
   const int Np = (a.N + 63) / 64 * 64;
   CUtensorMap gmap, wmap;
   cudaError_t err = make_f16_map(&gmap, a.gs, (uint64_t)a.T, 2 * (uint64_t)Np, kDxTok);
-  if (err == cudaSuccess) err = make_f16_map(&wmap, a.wt, (uint64_t)a.K, 2 * (uint64_t)Np, kDxCol);
+  if (err == cudaSuccess) err = make_f16_map(&wmap, a.wt, (uint64_t)a.K, 2 * (uint64_t)Np, COL);
   if (err != cudaSuccess) return err;
-  static int smem_set[64] = {0};
-  err = ensure_smem(k_lora_dx, kDxSmem, smem_set);
-  static std::atomic<int> regs{0};
-  if (err == cudaSuccess) err = launch_regs_ok(k_lora_dx, kDxLaunchRegs, regs);
+  return launch_cluster_pdl(k_lora_dx<COL>,
+                            dim3((unsigned)((a.K + COL - 1) / COL), (unsigned)((a.T + kDxTok - 1) / kDxTok), (unsigned)shares),
+                            dim3(kDxThreads), dim3(1, 1, (unsigned)shares), DxCfg<COL>::SMEM, s, a, gmap, wmap);
+}
+
+cudaError_t base_dx(const LoraArgs &a, int sms, cudaStream_t s) {
+  cudaError_t err = dx_ready<256>();
+  if (err == cudaSuccess) err = dx_ready<192>();
   if (err != cudaSuccess) return err;
-  const int n_tiles = Np / 64, w_tiles = n_tiles * (a.K / 64);
+  const int n_tiles = (a.N + 63) / 64, w_tiles = n_tiles * (a.K / 64);
   err = launch_pdl(k_lora_lay, dim3((unsigned)(w_tiles + a.T)), dim3(256), 0, s, a, w_tiles, n_tiles);
   if (err != cudaSuccess) return err;
-  return launch_pdl(k_lora_dx, dim3((unsigned)((a.K + kDxCol - 1) / kDxCol), (unsigned)((a.T + kDxTok - 1) / kDxTok)),
-                    dim3(kDxThreads), kDxSmem, s, a, gmap, wmap);
+  // The most CTAs per tile of 256 that all run at once, as long as each keeps
+  // four stages; where a tile is not shared out, 192 columns if their waves are
+  // shorter (512 tokens by 6144: 128 tiles of 192 in one wave, 96 of 256 in one
+  // too, but a third longer each).
+  const int64_t rows = (a.T + kDxTok - 1) / kDxTok, c256 = (a.K + 255) / 256, c192 = (a.K + 191) / 192;
+  static std::atomic<int> known[64][9];
+  int shares = 1;
+  for (int c = 2; c <= 8 && n_tiles / c >= 4; ++c)
+    if (rows * c256 <= max_clusters(k_lora_dx<256>, kDxThreads, DxCfg<256>::SMEM, c, known)) shares = c;
+  if (shares > 1) return dx_launch<256>(a, shares, s);
+  const int64_t w256 = (rows * c256 + sms - 1) / sms * 256, w192 = (rows * c192 + sms - 1) / sms * 192;
+  return w192 < w256 ? dx_launch<192>(a, 1, s) : dx_launch<256>(a, 1, s);
 }
 
 }  // namespace
@@ -467,7 +523,7 @@ cudaError_t launch_lora_bwd(const LoraArgs &a, int sms, cudaStream_t s) {
   if (err == cudaSuccess && a.n > 0 && a.dB != nullptr)
     err = a.u != nullptr ? outer(a, a.u, 1, a.g, a.N, a.dB, 1, s) : outer(a, a.us, 0, a.g, a.N, a.dB, 1, s);
   if (err != cudaSuccess || a.dx == nullptr || a.T == 0) return err;
-  err = base_dx(a, s);
+  err = base_dx(a, sms, s);
   if (err != cudaSuccess || a.n == 0) return err;
   return launch_lora_expand(a, a.v, a.A, false, a.K, a.dx, sms, s);
 }
