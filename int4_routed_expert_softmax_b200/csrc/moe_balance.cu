@@ -23,7 +23,7 @@
 namespace moe {
 namespace {
 
-constexpr int kFwdThreads = 256, kFwdWarps = kFwdThreads / 32;
+constexpr int kFwdThreads = 512, kFwdWarps = kFwdThreads / 32;
 constexpr int kBwdThreads = 256, kBwdWarps = kBwdThreads / 32;
 
 // Expert of a lane's i-th value; `sub`: the lane's place among its row's L.
@@ -41,7 +41,7 @@ __device__ __forceinline__ int expert_of(int i, int sub) {
 // more than a multiple of 32: four rows' 4-byte reads then use all banks).
 template <int L, int NV, int VEC, bool W2>
 struct RowRing {
-  static constexpr int R = NV <= 8 ? 4 : NV == 16 ? 3 : 2;  // turns of 32 NV words: two CTAs per SM hold theirs
+  static constexpr int R = NV <= 8 ? 3 : 2;
   static constexpr int kCols = L * NV, kWords = kCols + (W2 ? 96 : 32) + 8, kRows = 32 / L;
   static constexpr int kTotal = R * kRows * kWords;
   float *mine;  // this lane's row of slot 0
@@ -125,23 +125,24 @@ __device__ __forceinline__ float exp2_fast(float x) {
 // NaN and +inf give NaN.
 template <int L, int NV>
 __device__ __forceinline__ void softmax_row(f32x2 (&v)[NV / 2], float &inv) {
-  float m = -INFINITY;
+  // four chains each: a warp has little else to fill a dependent operation's wait
+  float ms[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
   for (int i = 0; i < NV / 2; ++i) {
     const float2 x = unpack2(v[i]);
-    m = fmaxf(fmaxf(m, x.x), x.y);
+    ms[i & 3] = fmaxf(fmaxf(ms[i & 3], x.x), x.y);
   }
-  m = row_max<L>(m);
+  float m = row_max<L>(fmaxf(fmaxf(ms[0], ms[1]), fmaxf(ms[2], ms[3])));
   if (m == -INFINITY) m = 0.0f;  // every term is then exp(-inf) = 0 (or NaN for a NaN)
   const f32x2 m2 = pack2(-m, -m), l2 = pack2(1.44269504f, 1.44269504f);
-  f32x2 s = 0ull;
+  f32x2 s[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
   for (int i = 0; i < NV / 2; ++i) {
     const float2 x = unpack2(mul2(add2(v[i], m2), l2));
     v[i] = pack2(exp2_fast(x.x), exp2_fast(x.y));
-    s = add2(s, v[i]);
+    s[i & 3] = add2(s[i & 3], v[i]);
   }
-  const float2 h = unpack2(s);
+  const float2 h = unpack2(add2(add2(s[0], s[1]), add2(s[2], s[3])));
   const float sum = row_add<L>(h.x + h.y);
   inv = sum == 0.0f ? 0.0f : __frcp_rn(sum);
 }
@@ -194,7 +195,7 @@ __device__ __forceinline__ float finish_expert(const BalanceArgs &a, int s, int 
 // both indexes never falling, so their sum is a slot of its own.  A call of one
 // CTA finishes the segments itself.
 template <int L, int NV, int VEC>
-__global__ void __launch_bounds__(kFwdThreads) k_balance_fwd(const BalanceArgs a) {
+__global__ void __launch_bounds__(kFwdThreads, NV <= 16 ? 2 : 1) k_balance_fwd(const BalanceArgs a) {
   extern __shared__ __align__(16) float bsm[];
   using Ring = RowRing<L, NV, VEC, false>;
   constexpr int R = Ring::R, kRows = Ring::kRows, kTurn = kFwdWarps * kRows;  // rows of the CTA per turn
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(1024) k_balance_join(const BalanceArgs a) {
 // its segment in registers.  The kept part (DW) is added in the row's own place
 // in the ring, where the gradient passes on its way out.
 template <int L, int NV, int VEC, bool DW>
-__global__ void __launch_bounds__(kBwdThreads) k_balance_bwd(const BalanceArgs a) {
+__global__ void __launch_bounds__(kBwdThreads, NV <= 16 ? 4 : 2) k_balance_bwd(const BalanceArgs a) {
   extern __shared__ __align__(16) float bsm[];
   using Ring = RowRing<L, NV, VEC, DW>;
   constexpr int R = Ring::R, kRows = Ring::kRows, kTurn = kBwdWarps * kRows;
@@ -428,10 +429,10 @@ __global__ void __launch_bounds__(kBwdThreads) k_balance_bwd(const BalanceArgs a
     __syncwarp();
     float inv;
     softmax_row<L, NV>(o, inv);
-    f32x2 dot2 = 0ull;
+    f32x2 dots[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-    for (int i = 0; i < NV / 2; ++i) dot2 = fma2(f[i], o[i], dot2);
-    const float2 h = unpack2(dot2);
+    for (int i = 0; i < NV / 2; ++i) dots[i & 3] = fma2(f[i], o[i], dots[i & 3]);
+    const float2 h = unpack2(add2(add2(dots[0], dots[1]), add2(dots[2], dots[3])));
     const float dot = row_add<L>(h.x + h.y) * inv;
     if (t >= s_begin && s < a.S && valid) {
       const float c = cs * inv;
@@ -547,18 +548,18 @@ cudaError_t bwd(const BalanceArgs &a, int grid, cudaStream_t s) {
 }
 
 // Lanes per row and values per lane: the smallest instance that holds the row.
-#define MOE_BALANCE_DISPATCH(fn)                    \
-  if (vec4(a)) {                                   \
-    if (a.E <= 64) return fn<8, 8, 4>(a, grid, s);   \
-    if (a.E <= 128) return fn<8, 16, 4>(a, grid, s); \
-    if (a.E <= 256) return fn<8, 32, 4>(a, grid, s); \
-    if (a.E <= 512) return fn<16, 32, 4>(a, grid, s); \
-    return fn<32, 32, 4>(a, grid, s);              \
-  }                                                \
-  if (a.E <= 64) return fn<8, 8, 1>(a, grid, s);     \
-  if (a.E <= 128) return fn<8, 16, 1>(a, grid, s);   \
-  if (a.E <= 256) return fn<8, 32, 1>(a, grid, s);   \
-  if (a.E <= 512) return fn<16, 32, 1>(a, grid, s);  \
+#define MOE_BALANCE_DISPATCH(fn)                     \
+  if (vec4(a)) {                                    \
+    if (a.E <= 64) return fn<8, 8, 4>(a, grid, s);    \
+    if (a.E <= 128) return fn<16, 8, 4>(a, grid, s);  \
+    if (a.E <= 256) return fn<16, 16, 4>(a, grid, s); \
+    if (a.E <= 512) return fn<32, 16, 4>(a, grid, s); \
+    return fn<32, 32, 4>(a, grid, s);               \
+  }                                                 \
+  if (a.E <= 64) return fn<8, 8, 1>(a, grid, s);      \
+  if (a.E <= 128) return fn<16, 8, 1>(a, grid, s);    \
+  if (a.E <= 256) return fn<16, 16, 1>(a, grid, s);   \
+  if (a.E <= 512) return fn<32, 16, 1>(a, grid, s);   \
   return fn<32, 32, 1>(a, grid, s);
 
 cudaError_t dispatch_fwd(const BalanceArgs &a, int grid, cudaStream_t s) { MOE_BALANCE_DISPATCH(fwd) }

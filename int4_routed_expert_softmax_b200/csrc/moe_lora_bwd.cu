@@ -184,20 +184,32 @@ __global__ void __launch_bounds__(256, 2) k_lora_outer(const LoraArgs a, const f
 __device__ __forceinline__ void lay_wt(const LoraArgs &a, int n_tile, int g) {
   __shared__ __half hi[64][72], lo[64][72];  // [k][n]
   const int n0 = n_tile * 64, G = a.K / 64;
-  const int tid = threadIdx.x, n = tid & 63, part = tid >> 6;  // 8 packed bytes each
-  uint2 w = make_uint2(0x88888888u, 0x88888888u);
-  float s = 0.0f;
-  if (n0 + n < a.N) {
-    w = __ldg(reinterpret_cast<const uint2 *>(a.W + (size_t)(n0 + n) * (a.K / 2) + (size_t)g * 32 + part * 8));
-    const __half *sc = reinterpret_cast<const __half *>(a.W + (size_t)a.N * (a.K / 2));
-    s = __half2float(sc[(size_t)(n0 + n) * G + g]) * a.wexp[n0 + n];
+  // a thread takes 4 packed bytes of two rows, so that it stores pairs
+  const int tid = threadIdx.x, n = (tid & 31) * 2, part = tid >> 5;
+  const __half *sc = reinterpret_cast<const __half *>(a.W + (size_t)a.N * (a.K / 2));
+  uint32_t w[2];
+  float s[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = n0 + n + h;
+    const bool in = row < a.N;
+    w[h] = in ? __ldg(reinterpret_cast<const uint32_t *>(a.W + (size_t)row * (a.K / 2) + (size_t)g * 32 + part * 4))
+              : 0x88888888u;
+    s[h] = in ? __half2float(sc[(size_t)row * G + g]) * a.wexp[row] : 0.0f;
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = ((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 255u;
-    const int k = part * 8 + i;
-    split_f16((float)((int)(b & 15u) - 8) * s, hi[k][n], lo[k][n]);
-    split_f16((float)((int)(b >> 4) - 8) * s, hi[k + 32][n], lo[k + 32][n]);
+  for (int i = 0; i < 4; ++i) {
+    const int k = part * 4 + i;
+    const uint32_t b0 = (w[0] >> (8 * i)) & 255u, b1 = (w[1] >> (8 * i)) & 255u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // low nibbles: element k, high: k + 32
+      const int v0 = (int)(h ? b0 >> 4 : b0 & 15u) - 8, v1 = (int)(h ? b1 >> 4 : b1 & 15u) - 8;
+      __half h0, l0, h1, l1;
+      split_f16((float)v0 * s[0], h0, l0);
+      split_f16((float)v1 * s[1], h1, l1);
+      *reinterpret_cast<__half2 *>(&hi[k + 32 * h][n]) = __halves2half2(h0, h1);
+      *reinterpret_cast<__half2 *>(&lo[k + 32 * h][n]) = __halves2half2(l0, l1);
+    }
   }
   __syncthreads();
   const int Np = (a.N + 63) / 64 * 64;
