@@ -145,7 +145,6 @@ __global__ void __launch_bounds__(256) k_lora_in(const LoraArgs a) {
   cluster.sync();  // the parts stay until they have been read
 }
 
-constexpr int kProjPre = 12;  // groups a warp holds in registers (12 * 8 warps * 64 = 6144 inputs)
 
 // The bytes of a 64-group that a lane holds of two rows, as the A operands of
 // the group's two blocks (low nibbles: block 0; high: block 1).
@@ -193,8 +192,11 @@ __host__ __device__ inline ProjLayout proj_layout(int K, int r, int NT) {
   return L;
 }
 
-template <int NT, bool BF16>
-__global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
+// PRE: the groups a warp loads into registers before its wait: 12 (6144 inputs)
+// or, up to 2048 inputs, 4, which leaves room for three CTAs per SM instead of two
+// (6144 rows are 384 CTAs: one wave).
+template <int NT, int PRE, bool BF16>
+__global__ void __launch_bounds__(256, PRE == 4 ? 3 : 2) k_lora_proj(const LoraArgs a) {
   extern __shared__ __align__(128) unsigned char psm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, q4 = lane & 3;
@@ -217,10 +219,10 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
     mbar_arrive_expect_tx(landed, bytes);
     bulk_g2s(psm + L.ws, a.W + (size_t)N * (a.K / 2) + (size_t)n0 * G * 2, bytes, landed);
   }
-  uint2 wl[kProjPre], wh[kProjPre];
+  uint2 wl[PRE], wh[PRE];
   auto load_w = [&](int i0) {
 #pragma unroll
-    for (int i = 0; i < kProjPre; ++i) {
+    for (int i = 0; i < PRE; ++i) {
       const int g = warp + 8 * (i0 + i);
       if (g < G) {
         wl[i] = __ldg(reinterpret_cast<const uint2 *>(Wl + (size_t)g * 32));
@@ -249,10 +251,10 @@ __global__ void __launch_bounds__(256) k_lora_proj(const LoraArgs a) {
   f32x2 acc[NT][2];
 #pragma unroll
   for (int j = 0; j < NT; ++j) acc[j][0] = acc[j][1] = 0ull;
-  for (int i0 = 0; warp + 8 * i0 < G; i0 += kProjPre) {
+  for (int i0 = 0; warp + 8 * i0 < G; i0 += PRE) {
     if (i0 > 0) load_w(i0);
 #pragma unroll
-    for (int i = 0; i < kProjPre; ++i) {
+    for (int i = 0; i < PRE; ++i) {
       const int g = warp + 8 * (i0 + i);
       if (g < G) {
         const float s0 = __half2float(ssc[gq * G + g]), s1 = __half2float(ssc[(gq + 8) * G + g]);
@@ -1010,19 +1012,24 @@ cudaError_t shrink(const LoraArgs &a, const float *src, int L, const void *M, fl
 template <bool BF16, bool TR>
 cudaError_t shrink_rank(const LoraArgs &a, const float *src, int L, const void *M, float *dst, float *user, int sms,
                         cudaStream_t s) {
-  // blocks of 32 of the rank: with 64 a warp's registers leave one CTA per SM (59 us against TODO)
+  // blocks of 32 of the rank: with 64 a warp's registers leave one CTA per SM (59 us against 38 for 2048 tokens of rank 64)
   if (a.r <= 16) return shrink<2, BF16, TR>(a, src, L, M, dst, user, sms, s);
   return shrink<4, BF16, TR>(a, src, L, M, dst, user, sms, s);
 }
 
-template <int NT, bool BF16>
-cudaError_t proj(const LoraArgs &a, cudaStream_t s) {
+template <int NT, int PRE, bool BF16>
+cudaError_t proj_launch(const LoraArgs &a, cudaStream_t s) {
   const size_t smem = (size_t)proj_layout(a.K, a.r, NT).total;
   static int smem_set[64] = {0};
-  cudaError_t err = ensure_smem(k_lora_proj<NT, BF16>, smem, smem_set);
+  cudaError_t err = ensure_smem(k_lora_proj<NT, PRE, BF16>, smem, smem_set);
   if (err != cudaSuccess) return err;
-  return launch_pdl(k_lora_proj<NT, BF16>, dim3((unsigned)((a.N + 15) / 16), (unsigned)((a.T + kProjTok - 1) / kProjTok)),
-                    dim3(256), smem, s, a);
+  return launch_pdl(k_lora_proj<NT, PRE, BF16>,
+                    dim3((unsigned)((a.N + 15) / 16), (unsigned)((a.T + kProjTok - 1) / kProjTok)), dim3(256), smem, s, a);
+}
+
+template <int NT, bool BF16>
+cudaError_t proj(const LoraArgs &a, cudaStream_t s) {
+  return a.K <= 2048 ? proj_launch<NT, 4, BF16>(a, s) : proj_launch<NT, 12, BF16>(a, s);
 }
 
 template <bool BF16>
