@@ -46,12 +46,24 @@ __device__ __forceinline__ void store_xs(float *xs, int t, int G, int k, float d
 // Q8_0 of four elements (8 lanes share a 32-block) and the block's scale.  The scale is the
 // product with fp32's 1/127, as tensor libraries evaluate a division by a
 // constant: at most a unit in the last place from amax / 127.
+// A code is the rounded quotient x / d; the product with 1 / d is off from it by
+// less than 127 * 2^-22, so it rounds to the same code unless it lies that near
+// a half-integer, where (and for a d whose inverse fp32 does not hold) the
+// division is made.
+__device__ __forceinline__ int quant1(float v, float d, float inv) {
+  const float r = v * inv;
+  float q = rintf(r);
+  if (!(fabsf(r - q) < 0.4999f)) q = rintf(fdiv(v, d));
+  return (int)fminf(fmaxf(q, -127.0f), 127.0f);
+}
 __device__ __forceinline__ int4 quant4(const float4 v, float &d) {
   float m = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
 #pragma unroll
   for (int off = 4; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
   d = fmul(m, 1.0f / 127.0f);
-  return make_int4(q8_code(v.x, d), q8_code(v.y, d), q8_code(v.z, d), q8_code(v.w, d));
+  if (!(d > 1e-30f)) return make_int4(q8_code(v.x, d), q8_code(v.y, d), q8_code(v.z, d), q8_code(v.w, d));
+  const float inv = __frcp_rn(d);
+  return make_int4(quant1(v.x, d, inv), quant1(v.y, d, inv), quant1(v.z, d, inv), quant1(v.w, d, inv));
 }
 
 // ===========================================================================

@@ -38,9 +38,7 @@ struct Tf32Pair {
 __device__ __forceinline__ Tf32Pair split_tf32(float v) {
   Tf32Pair p;
   p.hi = to_tf32(v);
-  // an infinite (or NaN) value has no rest: inf - inf would make it NaN
-  const float rest = v - __uint_as_float(p.hi);
-  p.lo = fabsf(v) <= 3.0e38f ? to_tf32(rest) : 0u;
+  p.lo = to_tf32(v - __uint_as_float(p.hi));  // NaN for an infinite v: its sums are not finite either way
   return p;
 }
 // D[16][8] += A[16][8] B[8][8]; lane = 4 g + q: a = A(g, q), A(g + 8, q),

@@ -55,13 +55,26 @@ __device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, b
                : "memory");
 }
 
+struct OuterSet {
+  const float *left, *right;
+  float *out;
+  int left_by_token, L, l_major;
+};
+
+// One launch makes both gradients: the first `first_blocks` column blocks those of
+// `first`, the rest those of `second`.
 template <int RM>
-__global__ void __launch_bounds__(256, 2) k_lora_outer(const LoraArgs a, const float *left, int left_by_token,
-                                                       const float *right, int L, float *out, int l_major) {
+__global__ void __launch_bounds__(256, 2) k_lora_outer(const LoraArgs a, const OuterSet first, const OuterSet second,
+                                                       int first_blocks) {
+  const bool is_first = (int)blockIdx.x < first_blocks;
+  const OuterSet set = is_first ? first : second;
+  const float *left = set.left, *right = set.right;
+  float *out = set.out;
+  const int left_by_token = set.left_by_token, L = set.L, l_major = set.l_major;
   extern __shared__ __align__(16) float osm[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, q = lane & 3;
   const int id = blockIdx.y, r = a.r;
-  const int l0 = blockIdx.x * kOuterL, lb = l0 + (warp & 1) * 32, j0 = blockIdx.z * kOuterJ, tw = warp >> 1;
+  const int l0 = ((int)blockIdx.x - (is_first ? 0 : first_blocks)) * kOuterL, lb = l0 + (warp & 1) * 32, j0 = blockIdx.z * kOuterJ, tw = warp >> 1;
   pdl_wait();
   const int p0 = a.off[id], p1 = a.off[id + 1], steps = (p1 - p0 + kOuterT - 1) / kOuterT;
   const float sc = left_by_token ? a.scale[id] : 1.0f;
@@ -184,19 +197,26 @@ __global__ void __launch_bounds__(256, 2) k_lora_outer(const LoraArgs a, const f
 __device__ __forceinline__ void lay_wt(const LoraArgs &a, int n_tile, int g) {
   __shared__ __half hi[64][72], lo[64][72];  // [k][n]
   const int n0 = n_tile * 64, G = a.K / 64;
-  // a thread takes 4 packed bytes of two rows, so that it stores pairs
+  // the packed tile and its scales come through shared memory (each sector is
+  // asked for once); then a thread takes 4 bytes of two rows, so that it stores
+  // pairs
+  __shared__ uint32_t raw[64][9];
+  __shared__ float sc[64];
   const int tid = threadIdx.x, n = (tid & 31) * 2, part = tid >> 5;
-  const __half *sc = reinterpret_cast<const __half *>(a.W + (size_t)a.N * (a.K / 2));
-  uint32_t w[2];
-  float s[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = n0 + n + h;
-    const bool in = row < a.N;
-    w[h] = in ? __ldg(reinterpret_cast<const uint32_t *>(a.W + (size_t)row * (a.K / 2) + (size_t)g * 32 + part * 4))
-              : 0x88888888u;
-    s[h] = in ? __half2float(sc[(size_t)row * G + g]) * a.wexp[row] : 0.0f;
+  if (tid < 128) {
+    const int row = tid >> 1, h = tid & 1;
+    uint4 v = make_uint4(0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u);
+    if (n0 + row < a.N)
+      v = __ldg(reinterpret_cast<const uint4 *>(a.W + (size_t)(n0 + row) * (a.K / 2) + (size_t)g * 32) + h);
+    raw[row][4 * h] = v.x, raw[row][4 * h + 1] = v.y, raw[row][4 * h + 2] = v.z, raw[row][4 * h + 3] = v.w;
+  } else if (tid < 192) {
+    const int row = n0 + tid - 128;
+    const __half *scales = reinterpret_cast<const __half *>(a.W + (size_t)a.N * (a.K / 2));
+    sc[tid - 128] = row < a.N ? __half2float(scales[(size_t)row * G + g]) * a.wexp[row] : 0.0f;
   }
+  __syncthreads();
+  const uint32_t w[2] = {raw[n][part], raw[n + 1][part]};
+  const float s[2] = {sc[n], sc[n + 1]};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int k = part * 4 + i;
@@ -464,20 +484,22 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
 }
 
 template <int RM>
-cudaError_t outer_rows(const LoraArgs &a, const float *left, int by_token, const float *right, int L, float *out,
-                       int l_major, cudaStream_t s) {
-  const dim3 grid((unsigned)((L + kOuterL - 1) / kOuterL), (unsigned)a.n, (unsigned)((a.r + kOuterJ - 1) / kOuterJ));
+cudaError_t outer_rows(const LoraArgs &a, const OuterSet &f, const OuterSet &g, cudaStream_t s) {
+  const int fb = (f.L + kOuterL - 1) / kOuterL, gb = (g.L + kOuterL - 1) / kOuterL;
+  const dim3 grid((unsigned)(fb + gb), (unsigned)a.n, (unsigned)((a.r + kOuterJ - 1) / kOuterJ));
   static int smem_set[64] = {0};
   const cudaError_t err = ensure_smem(k_lora_outer<RM>, kOuterSmem, smem_set);
   if (err != cudaSuccess) return err;
-  return launch_pdl(k_lora_outer<RM>, grid, dim3(256), kOuterSmem, s, a, left, by_token, right, L, out, l_major);
+  return launch_pdl(k_lora_outer<RM>, grid, dim3(256), kOuterSmem, s, a, f, g, fb);
 }
 
-cudaError_t outer(const LoraArgs &a, const float *left, int by_token, const float *right, int L, float *out,
-                  int l_major, cudaStream_t s) {
-  if (a.r <= 16) return outer_rows<1>(a, left, by_token, right, L, out, l_major, s);
-  if (a.r <= 32) return outer_rows<2>(a, left, by_token, right, L, out, l_major, s);
-  return outer_rows<4>(a, left, by_token, right, L, out, l_major, s);
+// dA and dB, whichever are asked for.
+cudaError_t outer(const LoraArgs &a, cudaStream_t s) {
+  OuterSet A{a.v, a.x, a.dA, 0, a.dA != nullptr ? a.K : 0, 0};
+  OuterSet B{a.u != nullptr ? a.u : a.us, a.g, a.dB, a.u != nullptr ? 1 : 0, a.dB != nullptr ? a.N : 0, 1};
+  if (a.r <= 16) return outer_rows<1>(a, A, B, s);
+  if (a.r <= 32) return outer_rows<2>(a, A, B, s);
+  return outer_rows<4>(a, A, B, s);
 }
 
 template <int COL>
@@ -531,9 +553,7 @@ cudaError_t launch_lora_bwd(const LoraArgs &a, int sms, cudaStream_t s) {
     err = launch_lora_shrink(a, a.g, a.N, a.B, true, a.v, nullptr, sms, s);
   if (err == cudaSuccess && any && a.dB != nullptr && a.u == nullptr)
     err = launch_lora_shrink(a, a.x, a.K, a.A, false, a.us, nullptr, sms, s);
-  if (err == cudaSuccess && a.n > 0 && a.dA != nullptr) err = outer(a, a.v, 0, a.x, a.K, a.dA, 0, s);
-  if (err == cudaSuccess && a.n > 0 && a.dB != nullptr)
-    err = a.u != nullptr ? outer(a, a.u, 1, a.g, a.N, a.dB, 1, s) : outer(a, a.us, 0, a.g, a.N, a.dB, 1, s);
+  if (err == cudaSuccess && a.n > 0 && (a.dA != nullptr || a.dB != nullptr)) err = outer(a, s);
   if (err != cudaSuccess || a.dx == nullptr || a.T == 0) return err;
   err = base_dx(a, sms, s);
   if (err != cudaSuccess || a.n == 0) return err;
