@@ -288,7 +288,8 @@ typedef struct moe_lora_dims {
 
 /* Device workspace of the calls below for up to T_max tokens (256-byte
  * aligned); with backward != 0 enough for both of them.  0 if the dims are not
- * accepted.  The backward's is about 4*N*(K + T_max) bytes. */
+ * accepted.  Forward: a few hundred KB for up to 64 tokens, about
+ * K*(4*T_max + 2*N) bytes beyond; backward: about 4*N*(K + T_max). */
 size_t moe_lora_workspace_bytes(const moe_lora_dims *dims, int32_t T_max, int32_t backward);
 
 /* out[t] = W^ x^_t + scale_a * B_a (A_a x_t), a = adapter[t]: x^ the Q8_0 codes
@@ -316,9 +317,11 @@ int moe_lora_forward(const moe_lora_dims *dims, int32_t T, const float *x, const
  * all fp32, overwritten (0 for an adapter without tokens), each may be NULL.
  * u_opt: the forward's, or NULL (A x is then computed again).  W^' g_t is
  * computed from 22-bit factors with fp32 sums.  Every pointer but scale,
- * adapter and u_opt is 16-byte aligned.  The workspace's first word is a
- * status word as in moe_ws_view (MOE_ERR_TIMEOUT if a bounded wait ran out,
- * dx is then not valid); the call resets it first. */
+ * adapter and u_opt is 16-byte aligned; no output overlaps an input or another
+ * output.  Sums over tokens take them in order, so the same call gives the same
+ * bits.  The workspace's first word is a status word as in the forward
+ * (MOE_ERR_TIMEOUT: dx is not valid); the call resets it first.  Capturable like
+ * the forward.  May use the forward's workspace if that was sized for it. */
 int moe_lora_backward(const moe_lora_dims *dims, int32_t T, const float *g, const float *x, const void *W,
                       const void *A, const void *B, const float *scale, const int32_t *adapter, const float *u_opt,
                       float *dx_opt, float *dA_opt, float *dB_opt, void *ws, size_t ws_bytes, void *stream);
