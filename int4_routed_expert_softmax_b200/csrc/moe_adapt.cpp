@@ -63,9 +63,9 @@ LoraLayout lora_layout(const moe_lora_dims &p, int T, bool backward) {
     L.xq = seg(kLoraSmallT * K);
     L.xs = seg((size_t)kLoraSmallT / 2 * (K / 64) * kXs * 4);
     if (T > kLoraSmallT) {
-      L.xh = seg(Tp * K * 4);
+      L.xh = seg(Tp * K * 2);
       L.wh = seg(N * K * 2);
-      L.xd = seg(K / 64 * Tp * 4);
+      L.xd = seg(K / 64 * Tp * 8);
       L.ws = seg(K / 64 * align_up(N, kLoraColTile) * 4);
     }
   }

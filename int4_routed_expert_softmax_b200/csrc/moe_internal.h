@@ -344,8 +344,8 @@ struct LoraArgs {
   // workspace; a position is a token's place among the tokens sorted by adapter
   int8_t *xq;               // small batches: [T][K] Q8_0 codes
   float *xs;                // and per two tokens and group [T / 2][K / 64][kXs] scales and starting values
-  __half *xh, *wh;          // larger ones: [T][2K] x^ over its group's scale, hi and lo, and [N][K] W's integers
-  float *xd, *ws;           // [K / 64][Tp] scales of x's groups, [K / 64][Nt] of W's
+  __half *xh, *wh;          // larger ones: [T][K] codes and [N][K] weights, integers in fp16
+  float *xd, *ws;           // [K / 64][Tp][2] scales of the codes' blocks, [K / 64][Nt] of W's groups
   int Nt;                   // row length of ws: N in whole tiles
   float *us;                // [Tp][r] scale * A x by sorted position (small batches: by token)
   int32_t *perm, *off, *tile;  // sorted order: token of each position, first position and tile per adapter

@@ -395,9 +395,9 @@ __device__ void sort_tokens(const LoraArgs &a, int *tab, int warps) {
 
 // The first kernel of a sorted call.  CTA 0 sorts the tokens by adapter; the
 // others take the powers of two of W's rows if `a.wexp` (the backward), else,
-// if there are any, they lay out the base product's operands: x^ over a scale
-// of each 64-group (a warp: 512 inputs of a token), W's integers, exact in fp16
-// (a warp: 1024 packed bytes), and in fp32 the scales of both, transposed.
+// if there are any, they lay out the base product's operands, integers exact in
+// fp16: the Q8_0 codes of x (a warp: 512 inputs of a token) and W (a warp: 1024
+// packed bytes); and in fp32 the scales of both, transposed.
 __global__ void __launch_bounds__(1024) k_lora_prep(const LoraArgs a, int warps) {
   extern __shared__ int tab[];  // [warps][n + 1]
   pdl_launch_dependents();
@@ -441,19 +441,12 @@ __global__ void __launch_bounds__(1024) k_lora_prep(const LoraArgs a, int warps)
         const int km = k + 128 * m;
         float d;
         const int4 q = quant4(v[m], d);
-        // the group's larger scale f comes out of it; what stays, at most 127
-        // times a ratio of at most 1, goes to fp16 hi + lo
-        const float f = fmaxf(d, __shfl_xor_sync(0xffffffffu, d, 8));
-        const float ratio = f > 0.0f ? fdiv(d, f) : 0.0f;
         if (km < a.K) {
-          const int qs[4] = {q.x, q.y, q.z, q.w};
-          __half h[4], l[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split_f16((float)qs[e] * ratio, h[e], l[e]);
-          __half *o = a.xh + (size_t)t * (2 * (size_t)a.K) + (km >> 6) * 128 + (km & 63);
-          *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(h);
-          *reinterpret_cast<uint2 *>(o + 64) = *reinterpret_cast<const uint2 *>(l);
-          if ((lane & 15) == 0) a.xd[(size_t)(km >> 6) * Tp + t] = f;
+          const __half2 h0 = __halves2half2(__int2half_rn(q.x), __int2half_rn(q.y));
+          const __half2 h1 = __halves2half2(__int2half_rn(q.z), __int2half_rn(q.w));
+          *reinterpret_cast<uint2 *>(a.xh + (size_t)t * a.K + km) =
+              make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+          if ((lane & 7) == 0) a.xd[((size_t)(km >> 6) * Tp + t) * 2 + ((km >> 5) & 1)] = d;
         }
       }
     } else if (i < nx + nw) {
@@ -645,38 +638,37 @@ __global__ void __launch_bounds__(256, 2) k_lora_shrink(const LoraArgs a, const 
 }
 
 // The base product on the fifth-generation tensor cores: tiles of 128 tokens
-// (TMEM lanes) by 256 rows of W (columns), in token order.  Per 64-group the
-// weights are integers, exact in fp16, and x^ over the group's scale f (the
-// larger of its two blocks') comes as fp16 hi + lo, 22 bits: eight MMAs of 16
-// and one accumulator, read out once per group as
-//   acc += s (f C)
-// in packed fp32 by the warps that hold the sums; a lane holds a token (its f),
-// the scales s come with the stage.  Two accumulators take turns.  Measured:
-// 1.01 us per group of a tile, 104 us for 2048 tokens by 2048 x 6144 (tensor pipe
-// 58 % busy).  The MMAs alone take 0.66, the copies alone 0.55, the sums alone
-// 0.62: what they share is shared memory (161 KB of operands and copies per
-// group, and the scales' reads).  One exact pass over the codes with an
-// accumulator per 32-block has half the MMAs but needs both halves of tensor
-// memory for one group, and then waits for every hand-over between the MMAs and
-// the sums: 0.9 us.  It is not taken, because here x^ costs K split over
-// clusters nothing: 203 tokens take 28 us against 36.
+// (TMEM lanes) by 256 rows of W (columns), in token order.  Codes and weights are
+// integers, exact in fp16, and a block of 32 of them (two MMAs of 16) sums to an
+// exact integer in the fp32 accumulator, so the only roundings are those of
+//   acc += s (S_0 d_0 + S_1 d_1)
+// per 64-group, in packed fp32 by the warps that read the accumulators: a lane
+// holds a token (its d), the scales s come with the stage.  Measured: 0.91 us per
+// 64-group of a 128 x 256 tile (1660 clocks), 100 us for 2048 tokens by 6144 x
+// 2048.  The MMAs are 512 of those clocks, the sums 768 (three packed operations
+// per two outputs); a group's accumulators fill tensor memory, so a half's next
+// MMAs wait for its sums, and the rest is that handing over.  x^ over its group's
+// scale as fp16 hi + lo needs one accumulator per group, with two taking turns,
+// but twice the MMAs and twice the bytes of x: 1.01 us per group.
 //
-// Eight warps take a quarter of the tokens by half of the columns each; warp 8
-// copies stages of one 64-group by TMA, warp 9 issues the MMAs.  With few tiles
-// a cluster of CTAs splits K.  The sums leave through shared memory, where each
-// CTA of the cluster joins its share of the columns in a fixed order.  Every
-// wait is bounded.
+// Eight warps take a quarter of the tokens by half of the columns each (sixteen
+// by a quarter: 1.07 us); warp 8 copies stages of one 64-group by TMA, warp 9
+// issues the MMAs.  The two column halves have accumulators of their own (two
+// blocks each), so that one half's MMAs run while the other's sums are read.
+// With few tiles a cluster of CTAs splits K (a group costs a CTA nearly the same
+// for 64 columns as for 256, so narrower tiles do not help).  The sums leave
+// through shared memory, where each CTA of the cluster joins its share of the
+// columns in a fixed order.  Every wait is bounded.
 //
 // The kernel reads nothing of the launch right before it (k_lora_shrink; that
 // one starts it after its own wait for k_lora_prep), so it runs beside it, and
 // waits for it only before it ends: k_lora_expand, which waits for this
 // kernel, then has both results.
-constexpr int kBaseN = 256, kBaseStages = 3;
-constexpr uint32_t kBaseA = 128 * 128, kBaseB = kBaseN * 128;  // hi or lo of x^, W
-constexpr uint32_t kBaseAB = 2 * kBaseA + kBaseB, kBaseS = kBaseN * 4, kBaseD = 128 * 4;
-constexpr uint32_t kBaseStage = kBaseAB + kBaseS + kBaseD;
+constexpr int kBaseN = 256, kBaseStages = 4;
+constexpr uint32_t kBaseA = 128 * 128, kBaseB = kBaseN * 128, kBaseS = kBaseN * 4, kBaseD = 128 * 8;
+constexpr uint32_t kBaseStage = kBaseA + kBaseB + kBaseS + kBaseD;
 constexpr size_t kBaseSmem = 1024 + 1024 + (size_t)kBaseStages * kBaseStage;  // alignment, barriers, stages
-static_assert((size_t)128 * (kBaseN + 4) * 4 <= (size_t)kBaseStages * kBaseAB, "the sums fit the stages");
+static_assert((size_t)128 * (kBaseN + 4) * 4 <= (size_t)kBaseStages * (kBaseA + kBaseB), "the sums fit the stages");
 // Launched at 168 registers a thread; the two epilogue warpgroups take 216, the
 // third (copies and MMAs) gives its own down to 72: 2 * 128 * 216 + 128 * 72 =
 // 384 * 168 (the host checks the launch count).
@@ -693,12 +685,12 @@ __global__ void __launch_bounds__(kBaseThreads, 1) k_lora_base(const LoraArgs a,
   constexpr int BN = kBaseN, HN = BN / 2, STG = kBaseStages;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t *full = reinterpret_cast<uint64_t *>(bsm), *empty = full + STG;
-  uint64_t *accfull = empty + STG, *accfree = accfull + 2, *done = accfree + 2;
+  uint64_t *accfull = empty + STG, *accfree = accfull + 2, *done = accfree + 2;  // per column half
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  unsigned char *buf = bsm + 1024;                                  // [STG][x^ hi, lo, W]
-  float *sbuf = reinterpret_cast<float *>(buf + STG * kBaseAB);     // [STG][BN] scales of W
-  float *dbuf = sbuf + STG * BN;                                    // [STG][128] scales of the tokens' groups
+  unsigned char *buf = bsm + 1024;                                       // [STG][A, B]
+  float *sbuf = reinterpret_cast<float *>(buf + STG * (kBaseA + kBaseB));  // [STG][BN] scales of W
+  float2 *dbuf = reinterpret_cast<float2 *>(sbuf + STG * BN);            // [STG][128] scales of the tokens' two blocks
   const int n0 = blockIdx.x * BN, t0 = blockIdx.y * 128, G = a.K / 64;
   const int shares = (int)gridDim.z, share = (int)blockIdx.z;
   const int g0 = (int)((int64_t)G * share / shares), S = (int)((int64_t)G * (share + 1) / shares) - g0;
@@ -706,11 +698,11 @@ __global__ void __launch_bounds__(kBaseThreads, 1) k_lora_base(const LoraArgs a,
     *abort_flag = 0;
     for (int s = 0; s < STG; ++s) {
       mbar_init(full + s, 1);
-      mbar_init(empty + s, 8);  // a warp that has seen the stage's MMAs done and read the scales
+      mbar_init(empty + s, 8);  // a warp that has seen a half's MMAs done and read the scales
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(accfull + s, 1);
-      mbar_init(accfree + s, 8);
+      mbar_init(accfree + s, 4);
     }
     mbar_init(done, 1);
     fence_barrier_init();
@@ -735,13 +727,12 @@ __global__ void __launch_bounds__(kBaseThreads, 1) k_lora_base(const LoraArgs a,
           break;
         }
         if (elect_one()) {
-          unsigned char *b = buf + s * kBaseAB;
+          unsigned char *b = buf + s * (kBaseA + kBaseB);
           mbar_arrive_expect_tx(full + s, kBaseStage);
-          tma_load_2d(b, &xmap, (g0 + j) * 128, t0, full + s);
-          tma_load_2d(b + kBaseA, &xmap, (g0 + j) * 128 + 64, t0, full + s);
-          tma_load_2d(b + 2 * kBaseA, &wmap, (g0 + j) * 64, n0, full + s);
+          tma_load_2d(b, &xmap, (g0 + j) * 64, t0, full + s);
+          tma_load_2d(b + kBaseA, &wmap, (g0 + j) * 64, n0, full + s);
           bulk_g2s(sbuf + s * BN, a.ws + (size_t)(g0 + j) * a.Nt + n0, kBaseS, full + s);
-          bulk_g2s(dbuf + s * 128, a.xd + (size_t)(g0 + j) * Tp + t0, kBaseD, full + s);
+          bulk_g2s(dbuf + s * 128, a.xd + ((size_t)(g0 + j) * Tp + t0) * 2, kBaseD, full + s);
         }
         __syncwarp();
         issued = j + 1;
@@ -750,29 +741,34 @@ __global__ void __launch_bounds__(kBaseThreads, 1) k_lora_base(const LoraArgs a,
         mbar_drain(full + j % STG, (uint32_t)(j / STG) & 1u, a.status, kDetLoraGemmDrain);
     }
     if (warp == kBaseMmaWarp) {
-      const uint32_t idesc = pf_idesc(BN);
+      const uint32_t idesc = pf_idesc(HN);
       const uint64_t ad0 = umma_desc_sw128(smem_u32(buf));
-      for (int j = 0; j < S; ++j) {
-        const int s = j % STG, set = j & 1;
-        if (!warp_wait(full + s, (uint32_t)(j / STG) & 1u, a.status, kDetLoraGemmFull, a.wait_limit) ||
-            (j >= 2 && !warp_wait(accfree + set, (uint32_t)(j / 2 - 1) & 1u, a.status, kDetLoraFree, a.wait_limit))) {
-          *abort_flag = 1;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + (uint32_t)(set * BN);
-        const uint64_t ad = ad0 + (uint64_t)((s * kBaseAB) >> 4), bd = ad + (uint64_t)((2 * kBaseA) >> 4);
-        if (elect_one()) {
+      bool bad = false;
+      for (int j = 0; j < S && !bad; ++j) {
+        const int s = j % STG;
+        bad = !warp_wait(full + s, (uint32_t)(j / STG) & 1u, a.status, kDetLoraGemmFull, a.wait_limit);
+        const uint64_t ad = ad0 + (uint64_t)((s * (kBaseA + kBaseB)) >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t o = (uint64_t)((k * 32) >> 4);
-            umma_f16(d, ad + o + (kBaseA >> 4), bd + o, idesc, (uint32_t)(k > 0));
-            umma_f16(d, ad + o, bd + o, idesc, 1u);
+        for (int h = 0; h < 2; ++h) {
+          if (!bad && j >= 1)
+            bad = !warp_wait(accfree + h, (uint32_t)(j - 1) & 1u, a.status, kDetLoraFree, a.wait_limit);
+          if (bad) break;
+          tc_fence_after();
+          const uint32_t d = tmem + (uint32_t)(h * 2 * HN);
+          const uint64_t bh = ad + (uint64_t)((kBaseA + h * HN * 128) >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const uint64_t o = (uint64_t)((b * 64) >> 4);
+              umma_f16(d + (uint32_t)(b * HN), ad + o, bh + o, idesc, 0u);
+              umma_f16(d + (uint32_t)(b * HN), ad + o + 2, bh + o + 2, idesc, 1u);
+            }
+            umma_commit(accfull + h);
           }
-          umma_commit(accfull + set);
+          __syncwarp();
         }
-        __syncwarp();
       }
+      if (bad) *abort_flag = 1;
       if (elect_one()) umma_commit(done);
       __syncwarp();
       mbar_drain(done, 0, a.status, kDetLoraGemmDrain);
@@ -785,44 +781,46 @@ __global__ void __launch_bounds__(kBaseThreads, 1) k_lora_base(const LoraArgs a,
     f32x2 acc[HN / 2];
 #pragma unroll
     for (int i = 0; i < HN / 2; ++i) acc[i] = 0ull;
-    const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * HN);
+    const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(half * 2 * HN);
     for (int j = 0; j < S; ++j) {
-      const int s = j % STG, set = j & 1;
-      const bool got = mbar_wait(accfull + set, (uint32_t)(j / 2) & 1u, a.status, kDetLoraAcc, a.wait_limit);
+      const int s = j % STG;
+      const bool got = mbar_wait(accfull + half, (uint32_t)j & 1u, a.status, kDetLoraAcc, a.wait_limit);
       if (!__all_sync(0xffffffffu, got)) {
         *abort_flag = 1;
         break;
       }
       tc_fence_after();
-      const uint32_t ta = at + (uint32_t)(set * BN);
-      // 32 columns at a time, the next ones on their way out of tensor memory
+      // 16 columns at a time, the next ones on their way out of tensor memory
       // meanwhile (its wait covers every load issued so far)
-      uint32_t v[2][32];
-      tmem_ld32(ta, v[0]);
+      uint32_t v0[2][16], v1[2][16];
+      tmem_ld16(at, v0[0]);
+      tmem_ld16(at + (uint32_t)HN, v1[0]);
       // the stage's scales landed with what the MMAs waited for: this phase is
       // complete, and testing it orders the copied bytes before the reads below
       mbar_try_wait(full + s, (uint32_t)(j / STG) & 1u);
-      const float f = dbuf[s * 128 + trow];
-      const f32x2 f2 = pack2(f, f);
+      const float2 d = dbuf[s * 128 + trow];
+      const f32x2 d0 = pack2(d.x, d.x), d1 = pack2(d.y, d.y);
       const float4 *sc = reinterpret_cast<const float4 *>(sbuf + s * BN + half * HN);
 #pragma unroll
-      for (int c = 0; c < HN; c += 32) {
-        const int b = (c >> 5) & 1;
+      for (int c = 0; c < HN; c += 16) {
+        const int b = (c >> 4) & 1;
         tmem_ld_wait();
-        if (c + 32 < HN) {
-          tmem_ld32(ta + (uint32_t)(c + 32), v[b ^ 1]);
+        if (c + 16 < HN) {
+          tmem_ld16(at + (uint32_t)(c + 16), v0[b ^ 1]);
+          tmem_ld16(at + (uint32_t)(HN + c + 16), v1[b ^ 1]);
         } else {
           // the accumulators are in registers: the MMAs may have them back
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(accfree + set);
+          if (lane == 0) mbar_arrive(accfree + half);
         }
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
+        for (int i = 0; i < 16; i += 4) {
           const float4 sv = sc[(c + i) / 4];
+          const f32x2 p0 = mul2(pack2i(v0[b][i], v0[b][i + 1]), d0), p1 = mul2(pack2i(v0[b][i + 2], v0[b][i + 3]), d0);
           f32x2 &a0 = acc[(c + i) / 2], &a1 = acc[(c + i) / 2 + 1];
-          a0 = fma2(mul2(pack2i(v[b][i], v[b][i + 1]), f2), pack2(sv.x, sv.y), a0);
-          a1 = fma2(mul2(pack2i(v[b][i + 2], v[b][i + 3]), f2), pack2(sv.z, sv.w), a1);
+          a0 = fma2(fma2(pack2i(v1[b][i], v1[b][i + 1]), d1, p0), pack2(sv.x, sv.y), a0);
+          a1 = fma2(fma2(pack2i(v1[b][i + 2], v1[b][i + 3]), d1, p1), pack2(sv.z, sv.w), a1);
         }
       }
       __syncwarp();
@@ -1074,7 +1072,7 @@ cudaError_t base(const LoraArgs &a, bool pdl, cudaStream_t s) {
   static std::atomic<int> regs{0};
   if (err == cudaSuccess) err = launch_regs_ok(k_lora_base, kBaseLaunchRegs, regs);
   CUtensorMap xmap, wmap;
-  if (err == cudaSuccess) err = make_f16_map(&xmap, a.xh, (uint64_t)a.T, 2 * (uint64_t)a.K, 128);
+  if (err == cudaSuccess) err = make_f16_map(&xmap, a.xh, (uint64_t)a.T, (uint64_t)a.K, 128);
   if (err == cudaSuccess) err = make_f16_map(&wmap, a.wh, (uint64_t)a.N, (uint64_t)a.K, kBaseN);
   if (err != cudaSuccess) return err;
   // The most CTAs per tile that all run at once, as long as each keeps four
