@@ -201,7 +201,7 @@ int moe_lora_backward(const moe_lora_dims *dims, int32_t T, const float *g, cons
   a.wt = at<void>(ws, L.wt);
   a.gs = at<void>(ws, L.gs);
   a.gexp = at<float>(ws, L.gexp);
-  a.wexp = at<float>(ws, L.wexp);
+  if (dx_opt != nullptr && T > 0) a.wexp = at<float>(ws, L.wexp);  // else W is not read, and may be NULL
   const int sms = moe_device_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
   return cuda_status(launch_lora_bwd(a, sms, static_cast<cudaStream_t>(stream)));

@@ -193,6 +193,21 @@ def test_backward_without_tokens():
     m.moe_lora_forward(p, e(0, 128), W, A, B, scale, torch.empty(0, dtype=torch.int32, device="cuda"), e(0, 64), ws)
 
 
+def test_backward_without_tokens_reads_no_input():
+    """No token: g, x, W and adapter may be null, the gradients are zeros."""
+    import ctypes
+    m = moe()
+    p = m.lora(128, 64, 3, 16, torch.float16)
+    _, _, A, B, scale, _, _ = inputs(4, 128, 64, 3, 16, torch.float16)
+    ws = dirty(m.alloc_lora_workspace(p, 4, backward=True))
+    dA, dB = torch.full((3, 16, 128), 7.0, device="cuda"), torch.full((3, 64, 16), 7.0, device="cuda")
+    rc = m.lib().moe_lora_backward(ctypes.byref(p), 0, None, None, None, A.data_ptr(), B.data_ptr(), scale.data_ptr(), None,
+                                   None, None, dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), ws.numel(),
+                                   torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0 and not dA.any() and not dB.any()
+
+
 @pytest.mark.parametrize("T", [6, 50])
 def test_adapter_gradients_by_differences(T):
     """sum(g out) is linear in A and in B: central differences over steps of a
