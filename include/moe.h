@@ -289,7 +289,7 @@ typedef struct moe_lora_dims {
 /* Device workspace of the calls below for up to T_max tokens (256-byte
  * aligned); with backward != 0 enough for both of them.  0 if the dims are not
  * accepted.  Forward: a few hundred KB for up to 64 tokens, about
- * K*(4*T_max + 2*N) bytes beyond; backward: about 4*N*(K + T_max). */
+ * 2*K*(T_max + N) bytes beyond; backward: about 4*N*(K + T_max). */
 size_t moe_lora_workspace_bytes(const moe_lora_dims *dims, int32_t T_max, int32_t backward);
 
 /* out[t] = W^ x^_t + scale_a * B_a (A_a x_t), a = adapter[t]: x^ the Q8_0 codes
@@ -298,8 +298,8 @@ size_t moe_lora_workspace_bytes(const moe_lora_dims *dims, int32_t T_max, int32_
  * a code may differ by one where x/d lies that close to a half-integer); the
  * adapters see x itself.
  * x [T][K] fp32, out [T][N] fp32, u_opt [T][rank] fp32 or NULL: A_a x_t (0 for
- * tokens without an adapter), which the backward takes.  x, W, A, B and out
- * 16-byte aligned; out and u_opt overlap no input.  Block sums are exact
+ * tokens without an adapter), which the backward takes.  x, W, A, B, out and
+ * u_opt 16-byte aligned; out and u_opt overlap no input.  Block sums are exact
  * integers; the other sums and the products with A and B are fp32 (22 bits or
  * more of every factor), in an order that depends on the shapes alone: the
  * same call gives the same bits.  Capturable in a CUDA graph after one call of
@@ -316,8 +316,8 @@ int moe_lora_forward(const moe_lora_dims *dims, int32_t T, const float *x, const
  *   dB_opt [n][N][rank] = scale_a * sum over them of g_t u_t'
  * all fp32, overwritten (0 for an adapter without tokens), each may be NULL.
  * u_opt: the forward's, or NULL (A x is then computed again).  W^' g_t is
- * computed from 22-bit factors with fp32 sums.  Every pointer but scale,
- * adapter and u_opt is 16-byte aligned; no output overlaps an input or another
+ * computed from 22-bit factors with fp32 sums.  Every pointer but scale
+ * and adapter is 16-byte aligned; no output overlaps an input or another
  * output.  Sums over tokens take them in order, so the same call gives the same
  * bits.  The workspace's first word is a status word as in the forward
  * (MOE_ERR_TIMEOUT: dx is not valid); the call resets it first.  Capturable like

@@ -156,7 +156,8 @@ int moe_lora_forward(const moe_lora_dims *dims, int32_t T, const float *x, const
   if (rc != MOE_OK) return rc;
   if (T == 0) return MOE_OK;
   if (!x || !W || !out || !ws || (dims->n_adapters > 0 && (!A || !B || !scale || !adapter))) return MOE_ERR_BAD_ARG;
-  if (!aligned(x, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(out, 16))
+  if (!aligned(x, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(out, 16) ||
+      !aligned(u_opt, 16))
     return MOE_ERR_BAD_ARG;
   if (!aligned(ws, 256)) return MOE_ERR_WORKSPACE;
   const LoraLayout L = lora_layout(*dims, T, false);
@@ -186,7 +187,7 @@ int moe_lora_backward(const moe_lora_dims *dims, int32_t T, const float *g, cons
   if (!ws || (dims->n_adapters > 0 && (!A || !B || !scale))) return MOE_ERR_BAD_ARG;
   if (T > 0 && (!g || !x || !W || (dims->n_adapters > 0 && !adapter))) return MOE_ERR_BAD_ARG;
   if (!aligned(g, 16) || !aligned(x, 16) || !aligned(W, 16) || !aligned(A, 16) || !aligned(B, 16) ||
-      !aligned(dx_opt, 16) || !aligned(dA_opt, 16) || !aligned(dB_opt, 16))
+      !aligned(u_opt, 16) || !aligned(dx_opt, 16) || !aligned(dA_opt, 16) || !aligned(dB_opt, 16))
     return MOE_ERR_BAD_ARG;
   if (!aligned(ws, 256)) return MOE_ERR_WORKSPACE;
   const LoraLayout L = lora_layout(*dims, T, true);

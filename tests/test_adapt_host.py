@@ -103,6 +103,13 @@ def test_balance_arguments(lib):
     assert balb(lib, d, T=0, logits=None, idx=None, counts=None, ntok=None, dloss=None, dlogits=None) == OK
 
 
+def test_lora_refuses_a_misaligned_u(lib):
+    """The backward reads u in 16-byte pieces."""
+    p = moe.lora(128, 64, 2, 8)
+    for at in (4096 + 4, 4096 + 8):
+        assert fwd(lib, p, u=at) == BAD_ARG and bwd(lib, p, u=at) == BAD_ARG
+
+
 def test_binding_refuses_host_tensors_and_wrong_types():
     p = moe.lora(128, 64, 2, 8)
     x, W = torch.zeros(4, 128), torch.zeros(64 * 64 + 256, dtype=torch.uint8)
