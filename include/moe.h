@@ -337,8 +337,10 @@ int moe_lora_backward(const moe_lora_dims *dims, int32_t T, const float *g, cons
  * means one segment of all T.  valid_opt [T] bytes or NULL: a token with 0 is
  * counted nowhere; neither is one outside every segment.  logits [T][E] and
  * idx [T][k] are moe_router_topk's; an idx outside [0, E) is a dropped pair and
- * is not counted.  S <= MOE_BALANCE_S_MAX.
+ * is not counted.  T <= MOE_BALANCE_T_MAX (counts stay within 32 bits, even of
+ * an expert listed in all of a token's 32 slots), S <= MOE_BALANCE_S_MAX.
  * ------------------------------------------------------------------------ */
+#define MOE_BALANCE_T_MAX (1 << 25)
 #define MOE_BALANCE_S_MAX 65535
 
 size_t moe_balance_workspace_bytes(const moe_dims *dims, int32_t T_max, int32_t S_max);

@@ -130,7 +130,7 @@ int check_balance(const moe_dims *dims, int32_t T, int32_t S, const int32_t *seg
   const int rc = moe_check_dims(dims);
   if (rc != MOE_OK) return rc;
   if (T < 0 || S < 1 || (S > 1 && seg_opt == nullptr)) return MOE_ERR_BAD_ARG;
-  if (S > MOE_BALANCE_S_MAX) return MOE_ERR_SHAPE;
+  if (T > MOE_BALANCE_T_MAX || S > MOE_BALANCE_S_MAX) return MOE_ERR_SHAPE;
   return MOE_OK;
 }
 
@@ -209,7 +209,9 @@ int moe_lora_backward(const moe_lora_dims *dims, int32_t T, const float *g, cons
 }
 
 size_t moe_balance_workspace_bytes(const moe_dims *dims, int32_t T_max, int32_t S_max) {
-  if (moe_check_dims(dims) != MOE_OK || T_max < 0 || S_max < 1 || S_max > MOE_BALANCE_S_MAX) return 0;
+  if (moe_check_dims(dims) != MOE_OK || T_max < 0 || T_max > MOE_BALANCE_T_MAX || S_max < 1 ||
+      S_max > MOE_BALANCE_S_MAX)
+    return 0;
   const int sms = moe_device_sms();
   return balance_layout(*dims, T_max, S_max, sms > 0 ? sms : 148).total;
 }

@@ -110,6 +110,14 @@ def test_lora_refuses_a_misaligned_u(lib):
         assert fwd(lib, p, u=at) == BAD_ARG and bwd(lib, p, u=at) == BAD_ARG
 
 
+def test_balance_refuses_more_tokens_than_its_indexes_hold(lib):
+    d, most = moe.dims(256, 128, 16, 2), 1 << 25
+    for T in (most + 1, 2 ** 31 - 1):
+        assert bal(lib, d, T=T) == SHAPE and balb(lib, d, T=T) == SHAPE
+        assert moe.moe_balance_workspace_bytes(d, T) == 0
+    assert moe.moe_balance_workspace_bytes(d, most, 65535) > 0
+
+
 def test_binding_refuses_host_tensors_and_wrong_types():
     p = moe.lora(128, 64, 2, 8)
     x, W = torch.zeros(4, 128), torch.zeros(64 * 64 + 256, dtype=torch.uint8)
