@@ -100,8 +100,7 @@ LoraArgs lora_args(const moe_lora_dims &p, int T, const float *x, const void *W,
 // Not the plan's own grid, which may fall by a few CTAs as T grows: a
 // workspace for T_max tokens serves every smaller batch.
 size_t balance_slots(int T, int S, int sms) {
-  const int64_t most = ((int64_t)T + kBalanceChunkMin - 1) / kBalanceChunkMin;
-  return (size_t)(most < kBalanceCtas * sms ? most : kBalanceCtas * sms) + (size_t)S + 1;
+  return (size_t)(T < kBalanceCtas * sms ? T : kBalanceCtas * sms) + (size_t)S + 1;
 }
 
 struct BalanceLayout {
@@ -228,13 +227,14 @@ int moe_balance_forward(const moe_dims *dims, int32_t T, int32_t S, const int32_
   if (sms <= 0) return MOE_ERR_CUDA;
   const BalanceLayout L = balance_layout(*dims, T, S, sms);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
-  const BalancePlan plan = balance_plan(T, sms);
+  const BalancePlan plan = balance_plan(T, S, sms);
   BalanceArgs a{};
   a.T = T;
   a.S = S;
   a.E = dims->E;
   a.k = dims->k;
   a.chunk = plan.chunk;
+  a.alone = plan.alone;
   a.seg = seg_opt;
   a.logits = logits;
   a.idx = idx;
@@ -248,7 +248,7 @@ int moe_balance_forward(const moe_dims *dims, int32_t T, int32_t S, const int32_
   a.part_n = at<int32_t>(ws, L.part_n);
   a.part_l = at<float>(ws, L.part_l);
   a.ticket = at<unsigned int>(ws, L.ticket);
-  return cuda_status(launch_balance_fwd(a, plan.grid, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_balance_fwd(a, plan.grid, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int moe_balance_backward(const moe_dims *dims, int32_t T, int32_t S, const int32_t *seg_opt, const float *logits,

@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kFwdThreads, NV <= 16 ? 2 : 1) k_balance_fwd(c
   __shared__ float sl[kFwdWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, sub = lane % L;
   const Ring ring(bsm + ((kFwdWarps + 1) * E + 3) / 4 * 4 + warp * Ring::kTotal, a, lane);
-  const bool alone = gridDim.x == 1;
+  const bool alone = a.alone;
   pdl_launch_dependents();
   const int t0 = min((int)((int64_t)blockIdx.x * a.chunk), a.T), t1 = min(t0 + a.chunk, a.T);
   // the first rows are brought near while the segments are looked up
@@ -229,7 +229,10 @@ __global__ void __launch_bounds__(kFwdThreads, NV <= 16 ? 2 : 1) k_balance_fwd(c
     const int b0 = max(sg.at(s), t0), b1 = min(sg.at(s + 1), t1);
     if (!alone) {
       if (sg.at(s) >= t1) break;
-      if (b0 >= b1) continue;  // empty, or none of its tokens here: its slot is never read
+      if (b0 >= b1) {  // empty: its slot is never read, nor are those of others that end here
+        s = max(s, sg.of(b0) - 1);
+        continue;
+      }
     }
     f32x2 acc[NV / 2];
 #pragma unroll
@@ -317,13 +320,13 @@ __global__ void __launch_bounds__(kFwdThreads, NV <= 16 ? 2 : 1) k_balance_fwd(c
 }
 
 // Joins the CTAs' sums: block (x, s) takes 32 experts of segment s, lane =
-// expert, the warps every 32nd slot, five of them at once; sums in 64 bits,
+// expert, of W warps each every W-th slot, five of them at once; sums in 64 bits,
 // always in the same order.  The last block of a segment adds the blocks'
 // shares of the loss.
 __global__ void __launch_bounds__(1024) k_balance_join(const BalanceArgs a) {
   __shared__ double rp[32][32];
   __shared__ int rc[32][32], rn[32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int s = blockIdx.y, e = blockIdx.x * 32 + lane;
   const Segments sg{a.seg, a.S, a.T};
   const int b0 = sg.at(s), b1 = sg.at(s + 1);
@@ -332,12 +335,12 @@ __global__ void __launch_bounds__(1024) k_balance_join(const BalanceArgs a) {
   int c = 0, n = 0;
   if (b0 < b1) {
     const int c1 = (b1 - 1) / a.chunk;
-    for (int q0 = b0 / a.chunk + warp; q0 <= c1; q0 += 5 * 32) {
+    for (int q0 = b0 / a.chunk + warp; q0 <= c1; q0 += 5 * warps) {
       float pv[5];
       int cv[5], nv[5];
 #pragma unroll
       for (int u = 0; u < 5; ++u) {
-        const int q = q0 + 32 * u;
+        const int q = q0 + warps * u;
         const size_t slot = (size_t)(q + s);
         const bool in = q <= c1;
         pv[u] = in && e < a.E ? a.part_p[slot * a.E + e] : 0.0f;
@@ -358,8 +361,8 @@ __global__ void __launch_bounds__(1024) k_balance_join(const BalanceArgs a) {
   __syncthreads();
   if (warp != 0) return;
   p = 0.0, c = 0, n = 0;
-#pragma unroll
-  for (int w = 0; w < 32; ++w) {
+#pragma unroll 4
+  for (int w = 0; w < warps; ++w) {
     p += rp[w][lane];
     c += rc[w][lane];
     n += rn[w];
@@ -569,28 +572,38 @@ cudaError_t dispatch_bwd(const BalanceArgs &a, int grid, cudaStream_t s) { MOE_B
 
 }  // namespace
 
-// Up to 64 tokens stay in one CTA (four rows a warp, one launch); beyond, up
-// to two CTAs per SM of 32 tokens at least.
-BalancePlan balance_plan(int T, int sms) {
+// Up to 64 tokens of one segment stay in one CTA (four rows a warp, one launch:
+// 4.5-6.8 us against 7.0-7.6 with the join).  Else up to two CTAs per SM, and the
+// join.  A CTA takes 16 tokens at least, or about a segment if those are shorter:
+// it works through its segments one after the other, 2.3 us each (64 tokens in 64
+// segments: 49 us at 16 tokens per CTA, 208 in a single one, 9 at one token).
+BalancePlan balance_plan(int T, int S, int sms) {
   BalancePlan p;
-  if (T <= 64) {
+  p.alone = T <= 64 && S == 1;
+  if (p.alone) {
     p.grid = 1;
     p.chunk = T > 0 ? T : 1;
     return p;
   }
   const int most = kBalanceCtas * sms;
+  const int least = T / S < 1 ? 1 : T / S < kBalanceChunkMin ? T / S : kBalanceChunkMin;
   p.chunk = (T + most - 1) / most;
-  if (p.chunk < kBalanceChunkMin) p.chunk = kBalanceChunkMin;
-  p.grid = (T + p.chunk - 1) / p.chunk;
+  if (p.chunk < least) p.chunk = least;
+  p.grid = T > 0 ? (T + p.chunk - 1) / p.chunk : 1;
   return p;
 }
 
-cudaError_t launch_balance_fwd(const BalanceArgs &a, int grid, cudaStream_t s) {
+cudaError_t launch_balance_fwd(const BalanceArgs &a, int grid, int sms, cudaStream_t s) {
   cudaError_t err = dispatch_fwd(a, grid, s);
-  if (err != cudaSuccess || grid == 1) return err;
+  if (err != cudaSuccess || a.alone) return err;
+  // 32 warps per block as long as all blocks run at once, for more segments down
+  // to 4 (2048 segments of one token: 45 us against 332 with 32 warps and 16 tokens per CTA)
+  const int blocks = (a.E + 31) / 32;
+  int warps = 32;
+  while (warps > 4 && (int64_t)blocks * a.S * warps > (int64_t)sms * 64) warps /= 2;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((a.E + 31) / 32), (unsigned)a.S);
-  cfg.blockDim = dim3(1024);
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)a.S);
+  cfg.blockDim = dim3((unsigned)warps * 32);
   cfg.stream = s;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -300,27 +300,29 @@ struct CombineArgs {
 // Balance loss of the router (moe_balance.cu).
 struct BalanceArgs {
   int T, S, E, k;
-  int chunk;               // consecutive tokens per CTA (forward) or per warp (backward)
+  int chunk;               // consecutive tokens per CTA
+  bool alone;              // forward: one CTA, which finishes the segments itself
   const int32_t *seg;      // [S + 1] token offsets or null (one segment: every token)
   const float *logits;     // [T][E]
   const int32_t *idx;      // [T][k], entries outside [0, E) are dropped pairs
   const uint8_t *valid;    // [T] or null
   int32_t *counts, *ntok;  // [S][E], [S]: written by the forward, read by the backward
   float *pmean, *loss;     // [S][E], [S]
-  float *part_p, *part_l;  // forward of more than one CTA: sums per (CTA, segment) slot, loss shares
+  float *part_p, *part_l;  // forward that is joined: sums per (CTA, segment) slot, loss shares
   int32_t *part_c, *part_n;
   unsigned int *ticket;    // [S]
   const float *dloss, *w, *dw;  // backward: [S], [T][k] or null, [T][k] or null
   float *dlogits;          // [T][E]
 };
-constexpr int kBalanceChunkMin = 16;  // tokens a CTA of the forward takes at least,
+constexpr int kBalanceChunkMin = 16;  // tokens a CTA of the forward takes at least (fewer of short segments),
 constexpr int kBalanceCtas = 2;       // and CTAs per SM at most
-// CTAs and tokens per CTA of the forward.
+// CTAs and tokens per CTA of the forward; alone: its one CTA finishes the segments.
 struct BalancePlan {
   int grid, chunk;
+  bool alone;
 };
-BalancePlan balance_plan(int T, int sms);
-cudaError_t launch_balance_fwd(const BalanceArgs &a, int grid, cudaStream_t s);
+BalancePlan balance_plan(int T, int S, int sms);
+cudaError_t launch_balance_fwd(const BalanceArgs &a, int grid, int sms, cudaStream_t s);
 cudaError_t launch_balance_bwd(const BalanceArgs &a, int sms, cudaStream_t s);
 
 // int4 projection with low-rank adapters (moe_lora.cu, moe_lora_bwd.cu).

@@ -101,6 +101,11 @@ def test_many_segments_and_long_batches(T, S):
     check(16, 2, inputs(T, 16, 2, S, True, seed=S))
 
 
+@pytest.mark.parametrize("T,S", [(0, 3), (1, 2), (1, 70), (16, 16), (40, 500), (64, 64), (300, 3000)])
+def test_segments_of_few_tokens_or_none(T, S):
+    check(33, 3, inputs(T, 33, 3, S, T > 3, seed=T + S))
+
+
 def test_without_weights_gradient():
     c = list(inputs(100, 32, 4, 3, True))
     c[5] = c[6] = None
