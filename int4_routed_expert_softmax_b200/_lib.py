@@ -4,7 +4,8 @@ device memory and streams; the functions take torch tensors and pass their
 data pointers and the current CUDA stream.
 
 Importing never falls back to anything else: if libmoe.so is missing or does not
-load, the first call raises."""
+load, the first call raises.  (_bind.so only makes the same argument checks in
+less time.)"""
 from __future__ import annotations
 
 import ctypes
@@ -322,88 +323,107 @@ def _adr(t, name: str, dtype, numel: int, dev: int):
     raise ValueError(f"{name} must be on device {dev}, is on {t.get_device()}")
 
 
+def _opt_adr(t, name: str, dtype, numel: int, dev: int):
+    """_adr; numel < 0: of an optional tensor of at least -1 - numel elements, None if it is None."""
+    if numel < 0:
+        if t is None:
+            return None
+        numel = -1 - numel
+    return _adr(t, name, dtype, numel, dev)
+
+
+def _adrs(dev: int, *spec):
+    """The addresses of (tensor, name, dtype, numel), ... as _opt_adr gives them."""
+    return tuple(_opt_adr(*spec[i:i + 4], dev) for i in range(0, len(spec), 4))
+
+
+try:  # the same checks in C++ (csrc/py/moe_bind.cpp): 3 us less per call; a refused tensor comes back here
+    from . import _bind
+    _bind.fallback(_on, _opt_adr)
+    _rows_on, _addresses = _bind.rows, _bind.addresses
+except ImportError:  # not built
+    _rows_on, _addresses = _on, _adrs
+
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
+_ADAPTER_DTYPES = (torch.float16, torch.bfloat16)
+
+
 def _raw_stream(stream, dev: int) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _lora_adr(p: MoeLoraDims, T: int, W, A, B, scale, adapter, dev: int):
-    N, K, n, r = p.N, p.K, p.n_adapters, p.rank
-    w = _adr(W, "W", torch.uint8, N * K // 2 + N * K // 32, dev)
-    if n == 0:
-        return w, None, None, None, None
-    dt = torch.bfloat16 if p.dtype == 1 else torch.float16
-    return (w, _adr(A, "A", dt, n * r * K, dev), _adr(B, "B", dt, n * N * r, dev),
-            _adr(scale, "scale", torch.float32, n, dev), _adr(adapter, "adapter", torch.int32, T, dev))
 
 
 def moe_lora_forward(p: MoeLoraDims, x, W, A, B, scale, adapter, out, ws, u=None, stream=None):
     """out[t] = W^ Q8_0(x_t) + scale_a B_a (A_a x_t), a = adapter[t] (none outside [0, n_adapters)).
     W: uint8, one int4 gs64 matrix (packed bytes, then scales); A [n][rank][K], B [n][N][rank];
     u [T][rank] (optional): A_a x_t, for the backward.  Every tensor on the current device."""
-    T, dev = _on(x, "x", p.K)
-    f32 = torch.float32
-    _check("moe_lora_forward", lib().moe_lora_forward(
-        p, T, x.data_ptr(), *_lora_adr(p, T, W, A, B, scale, adapter, dev), _adr(out, "out", f32, T * p.N, dev),
-        None if u is None else _adr(u, "u", f32, T * p.rank, dev), _adr(ws, "ws", torch.uint8, 0, dev), ws.numel(),
-        _raw_stream(stream, dev)))
+    K, N, n, r = p.K, p.N, p.n_adapters, p.rank
+    T, dev = _rows_on(x, "x", K)
+    w = (W, "W", _U8, N * K // 2 + N * K // 32)
+    o = (out, "out", _F32, T * N, u, "u", _F32, -1 - T * r, ws, "ws", _U8, 0)
+    if n == 0:
+        w, *o = _addresses(dev, *w, *o)
+        a = b = s = ids = None
+    else:
+        dt = _ADAPTER_DTYPES[p.dtype == 1]
+        w, a, b, s, ids, *o = _addresses(dev, *w, A, "A", dt, n * r * K, B, "B", dt, n * N * r, scale, "scale", _F32, n,
+                                         adapter, "adapter", _I32, T, *o)
+    _check("moe_lora_forward", lib().moe_lora_forward(p, T, x.data_ptr(), w, a, b, s, ids, *o, ws.numel(),
+                                                      _raw_stream(stream, dev)))
 
 
 def moe_lora_backward(p: MoeLoraDims, g, x, W, A, B, scale, adapter, ws, u=None, dx=None, dA=None, dB=None,
                       stream=None):
     """Gradients of moe_lora_forward for g [T][N]: dx [T][K], dA [n][rank][K], dB [n][N][rank], all float32,
     each optional.  u: the forward's A x (computed again without it).  Every tensor on the current device."""
-    T, dev = _on(x, "x", p.K)
-    if _on(g, "g", p.N)[0] != T:
+    K, N, n, r = p.K, p.N, p.n_adapters, p.rank
+    T, dev = _rows_on(x, "x", K)
+    if _rows_on(g, "g", N)[0] != T:
         raise ValueError(f"g has {g.shape[0]} rows, x has {T}")
-    f32, nr = torch.float32, p.n_adapters * p.rank
-    _check("moe_lora_backward", lib().moe_lora_backward(
-        p, T, g.data_ptr(), x.data_ptr(), *_lora_adr(p, T, W, A, B, scale, adapter, dev),
-        None if u is None else _adr(u, "u", f32, T * p.rank, dev),
-        None if dx is None else _adr(dx, "dx", f32, T * p.K, dev),
-        None if dA is None else _adr(dA, "dA", f32, nr * p.K, dev),
-        None if dB is None else _adr(dB, "dB", f32, nr * p.N, dev),
-        _adr(ws, "ws", torch.uint8, 0, dev), ws.numel(), _raw_stream(stream, dev)))
+    w = (W, "W", _U8, N * K // 2 + N * K // 32)
+    o = (u, "u", _F32, -1 - T * r, dx, "dx", _F32, -1 - T * K, dA, "dA", _F32, -1 - n * r * K, dB, "dB", _F32,
+         -1 - n * r * N, ws, "ws", _U8, 0)
+    if n == 0:
+        w, *o = _addresses(dev, *w, *o)
+        a = b = s = ids = None
+    else:
+        dt = _ADAPTER_DTYPES[p.dtype == 1]
+        w, a, b, s, ids, *o = _addresses(dev, *w, A, "A", dt, n * r * K, B, "B", dt, n * N * r, scale, "scale", _F32, n,
+                                         adapter, "adapter", _I32, T, *o)
+    _check("moe_lora_backward", lib().moe_lora_backward(p, T, g.data_ptr(), x.data_ptr(), w, a, b, s, ids, *o, ws.numel(),
+                                                        _raw_stream(stream, dev)))
 
 
 def moe_balance_workspace_bytes(d: MoeDims, T_max: int, S_max: int = 1) -> int:
     return int(lib().moe_balance_workspace_bytes(ctypes.byref(d), T_max, S_max))
 
 
-def _balance_adr(d: MoeDims, logits, idx, counts, ntok, seg, valid):
-    T, dev = _on(logits, "logits", d.E)
-    i32 = torch.int32
-    S = 1
-    sg = None
-    if seg is not None:
-        sg = _adr(seg, "seg", i32, 2, dev)
-        S = seg.numel() - 1
-    return (T, S, dev, sg, logits.data_ptr(), _adr(idx, "idx", i32, T * d.k, dev),
-            None if valid is None else _adr(valid, "valid", torch.uint8, T, dev),
-            _adr(counts, "counts", i32, S * d.E, dev), _adr(ntok, "ntok", i32, S, dev))
-
-
 def moe_balance_forward(d: MoeDims, logits, idx, counts, ntok, pmean, loss, ws, seg=None, valid=None, stream=None):
     """Balance loss per segment of packed tokens: counts [S][E] and ntok [S] int32, pmean [S][E] and
     loss [S] float32 from logits [T][E] and idx [T][k].  seg: [S+1] int32 token offsets (one segment
     without it); valid: [T] uint8, 0 for tokens that are not counted.  Every tensor on the current device."""
-    T, S, dev, *adr = _balance_adr(d, logits, idx, counts, ntok, seg, valid)
-    _check("moe_balance_forward", lib().moe_balance_forward(
-        d, T, S, *adr, _adr(pmean, "pmean", torch.float32, S * d.E, dev), _adr(loss, "loss", torch.float32, S, dev),
-        _adr(ws, "ws", torch.uint8, 0, dev), ws.numel(), _raw_stream(stream, dev)))
+    E = d.E
+    T, dev = _rows_on(logits, "logits", E)
+    S = seg.numel() - 1 if isinstance(seg, torch.Tensor) else 1
+    sg, *adr = _addresses(dev, seg, "seg", _I32, -3, idx, "idx", _I32, T * d.k, valid, "valid", _U8, -1 - T,
+                          counts, "counts", _I32, S * E, ntok, "ntok", _I32, S, pmean, "pmean", _F32, S * E,
+                          loss, "loss", _F32, S, ws, "ws", _U8, 0)
+    _check("moe_balance_forward", lib().moe_balance_forward(d, T, S, sg, logits.data_ptr(), *adr, ws.numel(),
+                                                            _raw_stream(stream, dev)))
 
 
 def moe_balance_backward(d: MoeDims, logits, idx, counts, ntok, dloss, dlogits, seg=None, valid=None, w=None,
                          dw=None, stream=None):
     """dlogits [T][E] for dloss [S] and, with w and dw [T][k], for the gradient of the kept weights."""
-    T, S, dev, *adr = _balance_adr(d, logits, idx, counts, ntok, seg, valid)
+    E, k = d.E, d.k
+    T, dev = _rows_on(logits, "logits", E)
+    S = seg.numel() - 1 if isinstance(seg, torch.Tensor) else 1
     if (w is None) != (dw is None):
         raise ValueError("w and dw come together")
-    f32 = torch.float32
-    _check("moe_balance_backward", lib().moe_balance_backward(
-        d, T, S, *adr, _adr(dloss, "dloss", f32, S, dev),
-        None if w is None else _adr(w, "w", f32, T * d.k, dev),
-        None if dw is None else _adr(dw, "dw", f32, T * d.k, dev), _adr(dlogits, "dlogits", f32, T * d.E, dev),
-        _raw_stream(stream, dev)))
+    sg, *adr = _addresses(dev, seg, "seg", _I32, -3, idx, "idx", _I32, T * k, valid, "valid", _U8, -1 - T,
+                          counts, "counts", _I32, S * E, ntok, "ntok", _I32, S, dloss, "dloss", _F32, S,
+                          w, "w", _F32, -1 - T * k, dw, "dw", _F32, -1 - T * k, dlogits, "dlogits", _F32, T * E)
+    _check("moe_balance_backward", lib().moe_balance_backward(d, T, S, sg, logits.data_ptr(), *adr,
+                                                              _raw_stream(stream, dev)))
 
 
 # ----------------------------------------------------------------- helpers

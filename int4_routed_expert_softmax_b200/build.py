@@ -1,4 +1,5 @@
-"""Builds libmoe.so (the C-ABI library) in-tree for sm_100a with nvcc.
+"""Builds libmoe.so (the C-ABI library) in-tree for sm_100a with nvcc, and the
+binding's argument checks (_bind.so) with g++ against torch's headers.
 
     python -m int4_routed_expert_softmax_b200.build [--force]
 """
@@ -15,6 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
+BIND_SRC = os.path.join(CSRC, "py", "moe_bind.cpp")
+BIND = os.path.join(PKG, "_bind.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
@@ -44,6 +47,19 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _build_bind(run) -> None:
+    import sysconfig
+
+    import torch
+    t = os.path.dirname(torch.__file__)
+    tmp = BIND + f".tmp{os.getpid()}"
+    run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + os.path.join(t, "include"),
+         "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
+         "-I" + sysconfig.get_paths()["include"], BIND_SRC, "-o", tmp, "-L" + os.path.join(t, "lib"), "-lc10",
+         "-ltorch_cpu", "-ltorch_python"])
+    os.replace(tmp, BIND)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -63,7 +79,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
             print(" ".join(cmd), flush=True)
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+            raise RuntimeError(f"{cmd[0]} failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return r.stdout + r.stderr
 
     with ThreadPoolExecutor(max_workers=min(8, max(1, len(jobs)))) as ex:
@@ -74,6 +90,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-lrt", "-ldl", "-lpthread"])
         os.replace(tmp, LIB)
+    if force or _stale(BIND, [BIND_SRC]):
+        _build_bind(run)
     return LIB
 
 

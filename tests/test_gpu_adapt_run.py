@@ -102,3 +102,47 @@ def test_step(T):
     assert abs(float(loss) - float(ref[3])) <= 2.0 ** -24 * (2 * E + 90 + T) * float(ref[3])
     size = float(ref[4].abs().max())
     assert float((dl.cpu().double() - ref[4]).abs().max()) <= 2.0 ** -24 * (3 * E + 120) * 4 * size
+
+
+@pytest.mark.parametrize("native", [True, False])
+def test_refusals_in_device_memory(native, monkeypatch):
+    """The binding's checks in C++ and in Python refuse the same tensors in the same words."""
+    import int4_routed_expert_softmax_b200 as m
+    from int4_routed_expert_softmax_b200 import _lib
+    if not native:
+        monkeypatch.setattr(_lib, "_rows_on", _lib._on)
+        monkeypatch.setattr(_lib, "_addresses", _lib._adrs)
+    else:
+        assert _lib._addresses is not _lib._adrs  # built
+    T, K, N, n, r = 4, 128, 64, 2, 8
+    p = m.lora(K, N, n, r)
+    z = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype, device="cuda")
+    good = dict(x=z(T, K), W=z(N * K // 2 + N * K // 32, dtype=torch.uint8), A=z(n, r, K, dtype=torch.bfloat16),
+                B=z(n, N, r, dtype=torch.bfloat16), scale=z(n), adapter=z(T, dtype=torch.int32), out=z(T, N) + 1,
+                ws=m.alloc_lora_workspace(p, T))
+    m.moe_lora_forward(p, **good)
+    assert not good["out"].any()
+    for name, bad, error in [
+            ("x", z(T, K + 64), r"x must be \[T\]\[128\]"), ("x", z(T, K).half(), "x must be torch.float32"),
+            ("x", z(K, T).t(), "x must be contiguous"), ("W", good["W"][:-1], "W has 4351 elements, needs at least 4352"),
+            ("A", good["A"].half(), "A must be torch.bfloat16"), ("B", good["B"].cpu(), "B must be in device memory"),
+            ("scale", None, "scale is required"), ("adapter", good["adapter"].long(), "adapter must be torch.int32"),
+            ("out", z(T, 2 * N)[:, ::2], "out must be contiguous"), ("u", z(T * r - 1), "u has 31 elements, needs at least 32"),
+            ("ws", None, "ws is required")]:
+        with pytest.raises(ValueError, match=error):
+            m.moe_lora_forward(p, **{**good, name: bad})
+    with pytest.raises(TypeError, match="scale must be a torch.Tensor"):
+        m.moe_lora_forward(p, **{**good, "scale": 1.0})
+    d = m.dims(256, 128, 16, 2)
+    i32 = lambda *s: z(*s, dtype=torch.int32)
+    bal = dict(logits=z(T, 16), idx=i32(T, 2), counts=i32(16), ntok=i32(1), pmean=z(16), loss=z(1),
+               ws=m.alloc_balance_workspace(d, T))
+    m.moe_balance_forward(d, **bal)
+    assert int(bal["ntok"]) == T
+    for name, bad, error in [("seg", i32(1), "seg has 1 elements, needs at least 2"),
+                             ("seg", i32(3), "counts has 16 elements, needs at least 32"),
+                             ("valid", z(T), "valid must be torch.uint8"), ("idx", i32(T, 1), "idx has 4 elements")]:
+        with pytest.raises(ValueError, match=error):
+            m.moe_balance_forward(d, **{**bal, name: bad})
+    with pytest.raises(TypeError, match="seg must be a torch.Tensor"):
+        m.moe_balance_forward(d, **{**bal, "seg": [0, 4]})
