@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(256, 2) k_lora_outer(const LoraArgs a, const O
 // ===========================================================================
 // operands of the base product
 // ===========================================================================
-// wt [K][2 Np]: per 64 rows of W 64 hi then 64 lo of column k, times wexp[n]; a
+// wt [K][2 Np]: per 32 rows of W 32 hi then 32 lo of column k, times wexp[n]; a
 // CTA transposes 64 rows by one 64-group.
 __device__ __forceinline__ void lay_wt(const LoraArgs &a, int n_tile, int g) {
   __shared__ __half hi[64][72], lo[64][72];  // [k][n]
@@ -235,8 +235,9 @@ __device__ __forceinline__ void lay_wt(const LoraArgs &a, int n_tile, int g) {
   const int Np = (a.N + 63) / 64 * 64;
   __half *wt = static_cast<__half *>(a.wt);
   for (int i = tid; i < 64 * 16; i += 256) {
-    const int k = i >> 4, c = i & 15;  // 16-byte pieces: 8 of hi, 8 of lo
-    const __half *src = c < 8 ? &hi[k][c * 8] : &lo[k][(c - 8) * 8];
+    const int k = i >> 4, c = i & 15;  // 16-byte pieces: 4 of hi, 4 of lo, twice
+    const int from = (c >> 3) * 32 + (c & 3) * 8;
+    const __half *src = (c & 4) == 0 ? &hi[k][from] : &lo[k][from];
     *reinterpret_cast<uint4 *>(wt + ((size_t)g * 64 + k) * (2 * (size_t)Np) + (size_t)n0 * 2 + c * 8) =
         *reinterpret_cast<const uint4 *>(src);
   }
@@ -272,9 +273,9 @@ __device__ __forceinline__ void lay_g(const LoraArgs &a, int t) {
     __half h[4], l[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) split_f16(v[i], h[i], l[i]);
-    __half *o = row + (n >> 6) * 128 + (n & 63);
+    __half *o = row + (n >> 5) * 64 + (n & 31);
     *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(h);
-    *reinterpret_cast<uint2 *>(o + 64) = *reinterpret_cast<const uint2 *>(l);
+    *reinterpret_cast<uint2 *>(o + 32) = *reinterpret_cast<const uint2 *>(l);
   }
 }
 
@@ -286,8 +287,8 @@ __global__ void __launch_bounds__(256) k_lora_lay(const LoraArgs a, int w_tiles,
 }
 
 // ===========================================================================
-// dx = g W^: tiles of 128 tokens by COL inputs.  Warp 8 loads (TMA, two stages
-// of 64 of the N reduction: 128 + COL rows of hi and lo), warp 9 issues the
+// dx = g W^: tiles of 128 tokens by COL inputs.  Warp 8 loads (TMA, four stages
+// of 32 of the N reduction: 128 + COL rows of 32 hi and 32 lo), warp 9 issues the
 // MMAs, warps 0-7 hold the sums in registers: a warp has one quarter of the
 // tokens (its TMEM lanes) by half of the inputs.  They add the accumulator every
 // kDxFlush stages, two accumulators taking turns, because the tensor cores
@@ -297,12 +298,12 @@ __global__ void __launch_bounds__(256) k_lora_lay(const LoraArgs a, int w_tiles,
 // fixed order.  Every wait is bounded.
 // ===========================================================================
 constexpr int kDxTok = 128;
-constexpr int kDxStages = 2;
-constexpr int kDxFlush = 2;
-constexpr uint32_t kDxA = kDxTok * 128;  // one of hi, lo
+constexpr int kDxStages = 4;
+constexpr int kDxFlush = 4;
+constexpr uint32_t kDxA = kDxTok * 128;  // hi and lo
 template <int COL>
 struct DxCfg {
-  static constexpr uint32_t B = COL * 128, STAGE = 2 * (kDxA + B);
+  static constexpr uint32_t B = COL * 128, STAGE = kDxA + B;
   static constexpr size_t SMEM = 1024 + (size_t)kDxStages * STAGE + 1024;  // barriers, stages, alignment
   static_assert((size_t)kDxTok * (COL + 4) * 4 <= (size_t)kDxStages * STAGE, "the sums fit the stages");
 };
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   unsigned char *buf = dsm + 1024;
   const int k0 = blockIdx.x * COL, t0 = blockIdx.y * kDxTok;
-  const int shares = (int)gridDim.z, share = (int)blockIdx.z, all = (a.N + 63) / 64;
+  const int shares = (int)gridDim.z, share = (int)blockIdx.z, all = (a.N + 63) / 64 * 2;
   const int s0 = (int)((int64_t)all * share / shares), S = (int)((int64_t)all * (share + 1) / shares) - s0;
   const int C = (S + kDxFlush - 1) / kDxFlush;
   if (threadIdx.x == 0) {
@@ -367,10 +368,8 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
         if (elect_one()) {
           unsigned char *b = buf + s * Cfg::STAGE;
           mbar_arrive_expect_tx(full + s, Cfg::STAGE);
-          tma_load_2d(b, &gmap, (s0 + j) * 128, t0, full + s);
-          tma_load_2d(b + kDxA, &gmap, (s0 + j) * 128 + 64, t0, full + s);
-          tma_load_2d(b + 2 * kDxA, &wmap, (s0 + j) * 128, k0, full + s);
-          tma_load_2d(b + 2 * kDxA + Cfg::B, &wmap, (s0 + j) * 128 + 64, k0, full + s);
+          tma_load_2d(b, &gmap, (s0 + j) * 64, t0, full + s);
+          tma_load_2d(b + kDxA, &wmap, (s0 + j) * 64, k0, full + s);
         }
         __syncwarp();
         issued = j + 1;
@@ -392,14 +391,14 @@ __global__ void __launch_bounds__(kDxThreads, 1) k_lora_dx(const LoraArgs a, con
         }
         tc_fence_after();
         const uint32_t d = tmem + (uint32_t)(c & 1) * kDxAcc;
-        const uint64_t ad = ad0 + (uint64_t)((s * Cfg::STAGE) >> 4), bd = ad + (uint64_t)((2 * kDxA) >> 4);
+        const uint64_t ad = ad0 + (uint64_t)((s * Cfg::STAGE) >> 4), bd = ad + (uint64_t)(kDxA >> 4);
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint64_t o = (uint64_t)((k * 32) >> 4);
-            umma_f16(d, ad + o, bd + o + (Cfg::B >> 4), idesc, (uint32_t)(!first || k > 0));
-            umma_f16(d, ad + o + (kDxA >> 4), bd + o, idesc, 1u);
-            umma_f16(d, ad + o, bd + o, idesc, 1u);
+          for (int k = 0; k < 2; ++k) {
+            const uint64_t hi = (uint64_t)((k * 32) >> 4), lo = hi + (64 >> 4);  // the row's 32 hi, then its 32 lo
+            umma_f16(d, ad + hi, bd + lo, idesc, (uint32_t)(!first || k > 0));
+            umma_f16(d, ad + lo, bd + hi, idesc, 1u);
+            umma_f16(d, ad + hi, bd + hi, idesc, 1u);
           }
           umma_commit(empty + s);
           if (j % kDxFlush == kDxFlush - 1 || j == S - 1) umma_commit(accfull + (c & 1));
