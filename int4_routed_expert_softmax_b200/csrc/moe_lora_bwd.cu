@@ -295,7 +295,9 @@ __global__ void __launch_bounds__(256) k_lora_lay(const LoraArgs a, int w_tiles,
 // truncate (one accumulator over N = 6144 was off by 2.2e-5; 24 MMAs lose 4e-7).
 // With few tiles a cluster of CTAs splits N; the sums leave through shared
 // memory, where each CTA of the cluster joins its share of the columns in a
-// fixed order.  Every wait is bounded.
+// fixed order.  Every wait is bounded.  Measured (2048 tokens, N = 6144, K = 2048):
+// 120 us, tensor pipe 79 % busy; two stages of 64, in the same shared memory,
+// keep fewer bytes on their way: 129 us, 72 %.
 // ===========================================================================
 constexpr int kDxTok = 128;
 constexpr int kDxStages = 4;
